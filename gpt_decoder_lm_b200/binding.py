@@ -27,6 +27,7 @@ GPT_PATH_GEMM_TC, GPT_PATH_ATTN_TC = 1, 2
 STATUS = ["GPT_OK", "GPT_ERR_INVALID_ARG", "GPT_ERR_CONFIG", "GPT_ERR_WORKSPACE_TOO_SMALL", "GPT_ERR_CUDA",
           "GPT_ERR_TOKEN_RANGE", "GPT_ERR_NONFINITE", "GPT_ERR_STATE", "GPT_ERR_UNSUPPORTED", "GPT_ERR_TIMEOUT"]
 FLAG_TOKEN, FLAG_LOSS, FLAG_NORM, FLAG_TIMEOUT = 1, 2, 4, 8
+FLAG_BLOCK_RANGE, FLAG_CACHE_FULL, FLAG_ROW_RANGE = 16, 32, 64
 
 
 class GptConfig(C.Structure):
@@ -38,6 +39,15 @@ class GptConfig(C.Structure):
         ("beta2", C.c_float), ("eps", C.c_float), ("weight_decay", C.c_float), ("grad_clip", C.c_float),
         ("decay_1d", C.c_int32), ("recompute", C.c_int32), ("dropout_seed", C.c_uint64),
         ("init_std", C.c_double), ("zero_world", C.c_int32), ("zero_rank", C.c_int32),
+    ]
+
+
+class Kv8CacheStruct(C.Structure):  # gpt_kv8_cache
+    _fields_ = [
+        ("n_seq", C.c_int32), ("n_head_kv", C.c_int32), ("head_dim", C.c_int32), ("block_tokens", C.c_int32),
+        ("n_blocks", C.c_int32), ("max_blocks", C.c_int32), ("d_k", C.c_void_p), ("d_v", C.c_void_p),
+        ("d_k_scale", C.c_void_p), ("d_v_scale", C.c_void_p), ("d_weight", C.c_void_p), ("d_table", C.c_void_p),
+        ("d_len", C.c_void_p), ("d_flags", C.c_void_p),
     ]
 
 
@@ -80,6 +90,11 @@ _PROTOS = {
     "gpt_eval_loss": (I32, [P, P, U64, U64, I32, P]),
     "gpt_sample": (I32, [P, I32, I32, I32, I64, F32, I32, F32, P, P, P]),
     "gpt_generate": (I32, [P, P, I32, I32, F32, I32, F32, P, P]),
+    "gpt_kv8_append": (I32, [P, P, I32, I32, I32, P, I64, P, I64, P]),
+    "gpt_kv8_attention": (I32, [P, P, I32, I32, I32, I32, P, I64, F32, I32, P, I64, P, P]),
+    "gpt_kv8_accumulate": (I32, [P, P, I32, I32, I32, I32, P, I64, F32, I32, P, P]),
+    "gpt_kv8_evict": (I32, [P, P, I32, I32, I32, P, P]),
+    "gpt_kv8_advance": (I32, [P, P, I32, I32, I32, P]),
     "gpt_lora_workspace_bytes": (I32, [P, I32, I32, P]),
     "gpt_lora_attach": (I32, [P, I32, F32, I32, P, P, SZ]),
     "gpt_lora_detach": (I32, [P]),
@@ -499,6 +514,153 @@ def sample(logits, temperature: float, top_k: int, top_p: float, uniform, out, V
     st = stream if stream is not None else torch.cuda.current_stream().cuda_stream
     _check(lib().gpt_sample(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, rows, V or ld, ld, temperature,
                             top_k, top_p, _ptr(uniform), _ptr(out), st), None, "sample")
+
+
+def _require(cond: bool, msg: str):
+    if not cond:
+        raise GptError(1, msg)
+
+
+class KV8Cache:
+    """An 8-bit key / value cache (gpt_kv8_cache) in the caller's tensors.
+
+    k, v: uint8 or float8_e4m3fn [n_blocks, n_head_kv, block_tokens, head_dim];
+    k_scale, v_scale: float32 [n_blocks, n_head_kv]; table: int32 [n_seq,
+    max_blocks]; length: int32 [n_seq]; weight (needed for accumulate and
+    evict): float32 [n_blocks, n_head_kv, block_tokens]; flags: int32 [1].  All
+    contiguous, on one device.  ``allocate`` makes them, with the blocks dealt
+    out in order.  Calls run on the device's current stream."""
+
+    def __init__(self, k, v, k_scale, v_scale, table, length, weight=None, flags=None):
+        import torch
+        e4m3 = torch.float8_e4m3fn
+        _require(k.dim() == 4 and table.dim() == 2, "kv8: k is [blocks, heads, tokens, dim], table [sequences, blocks]")
+        for t, shape, dtypes, name in ((k, k.shape, (torch.uint8, e4m3), "k"), (v, k.shape, (torch.uint8, e4m3), "v"),
+                                       (k_scale, k.shape[:2], (torch.float32,), "k_scale"),
+                                       (v_scale, k.shape[:2], (torch.float32,), "v_scale"),
+                                       (table, table.shape, (torch.int32,), "table"),
+                                       (length, table.shape[:1], (torch.int32,), "length"),
+                                       (weight, k.shape[:3], (torch.float32,), "weight"),
+                                       (flags, (1,), (torch.int32,), "flags")):
+            if t is not None:
+                _require(tuple(t.shape) == tuple(shape) and t.dtype in dtypes and t.is_contiguous() and
+                         t.device == k.device, f"kv8: {name} has another shape, type, layout or device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.length, self.weight, self.flags, self.device = length, weight, flags, k.device
+        self.n_seq, self.n_head_kv, self.head_dim = table.shape[0], k.shape[1], k.shape[3]
+        self._c = Kv8CacheStruct(table.shape[0], k.shape[1], k.shape[3], k.shape[2], k.shape[0], table.shape[1],
+                                 _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), _ptr(table),
+                                 _ptr(length), _ptr(flags))
+        self._ref = C.addressof(self._c)
+        self._lib = lib()
+        self._table = table
+
+    @classmethod
+    def allocate(cls, n_seq, n_head_kv, head_dim, block_tokens, max_blocks, n_blocks=None, weight=False, device="cuda"):
+        """A cache with memory of its own: empty, sequence s at blocks s * max_blocks .."""
+        import torch
+        n = n_seq * max_blocks if n_blocks is None else n_blocks
+        _require(n >= n_seq * max_blocks, "kv8: fewer blocks than the table needs")
+
+        def zeros(*shape, dtype=torch.float32):
+            return torch.zeros(*shape, dtype=dtype, device=device)
+        shape = (n, n_head_kv, block_tokens, head_dim)
+        table = torch.arange(n_seq * max_blocks, dtype=torch.int32, device=device).reshape(n_seq, max_blocks)
+        return cls(zeros(*shape, dtype=torch.uint8), zeros(*shape, dtype=torch.uint8), zeros(n, n_head_kv),
+                   zeros(n, n_head_kv), table, zeros(n_seq, dtype=torch.int32),
+                   zeros(*shape[:3]) if weight else None, zeros(1, dtype=torch.int32))
+
+    @property
+    def table(self):
+        return self._table
+
+    @table.setter
+    def table(self, t):
+        import torch
+        _require(t.dim() == 2 and t.shape[0] == self.n_seq and t.dtype == torch.int32 and t.is_contiguous() and
+                 t.device == self.device, "kv8: table has another shape, type, layout or device")
+        self._table = t
+        self._c.d_table, self._c.max_blocks = _ptr(t), t.shape[1]
+
+    def _call(self, what, name, *args):
+        """The library's call on the tensors' device and its current stream."""
+        import torch
+        stream = torch.cuda.current_stream(self.device).cuda_stream
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                st = getattr(self._lib, name)(self._ref, *args, stream)
+        else:
+            st = getattr(self._lib, name)(self._ref, *args, stream)
+        if st:
+            _check(st, None, what)
+
+    def _rows(self, x, heads, name):
+        """Pitch and type (1: bf16) of rows [n, heads, head_dim] whose heads are contiguous."""
+        import torch
+        _require(x.dim() == 3 and (heads is None or x.shape[1] == heads) and x.shape[2] == self.head_dim and
+                 x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == self.head_dim) and
+                 x.dtype in (torch.bfloat16, torch.float32) and x.device == self.device,
+                 f"kv8: {name} is [rows, heads, head_dim] of bfloat16 or float32 with contiguous heads, on the cache's device")
+        ld = x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1] * x.shape[2])
+        _require(ld >= x.shape[1] * x.shape[2], f"kv8: the rows of {name} overlap")
+        return ld, 1 if x.dtype == torch.bfloat16 else 0
+
+    def _start(self, start):
+        import torch
+        if start is not None:
+            _require(start.dtype == torch.int32 and tuple(start.shape) == (self.n_seq + 1,) and start.is_contiguous() and
+                     start.device == self.device, "kv8: start is int32 [n_seq + 1] on the cache's device")
+            return start.data_ptr()
+        return None
+
+    def append(self, k, v, start=None, max_new=1):
+        """gpt_kv8_append: k, v [rows, n_head_kv, head_dim], one type."""
+        k_ld, b = self._rows(k, self.n_head_kv, "k")
+        v_ld, _ = self._rows(v, self.n_head_kv, "v")
+        _require(v.dtype == k.dtype and v.shape[0] == k.shape[0], "kv8: k and v have the same rows and type")
+        self._call("kv8_append", "gpt_kv8_append", self._start(start), k.shape[0], max_new, b, k.data_ptr(), k_ld,
+                   v.data_ptr(), v_ld)
+
+    def attention(self, q, out, start=None, max_new=1, lse=None, scale=None, max_len=0):
+        """gpt_kv8_attention: q, out [rows, n_head, head_dim], one type; lse (optional) float32 [rows, n_head].
+        scale: 1 / sqrt(head_dim) where None."""
+        q_ld, b = self._rows(q, None, "q")
+        o_ld, _ = self._rows(out, q.shape[1], "out")
+        _require(out.dtype == q.dtype and out.shape[0] == q.shape[0], "kv8: q and out have the same rows and type")
+        self._call("kv8_attention", "gpt_kv8_attention", self._start(start), q.shape[0], max_new, q.shape[1], b,
+                   q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, out.data_ptr(), o_ld,
+                   self._lse(lse, q))
+
+    def accumulate(self, q, lse, start=None, max_new=1, scale=None, max_len=0):
+        """gpt_kv8_accumulate, with the lse that ``attention`` gave for q."""
+        q_ld, b = self._rows(q, None, "q")
+        self._call("kv8_accumulate", "gpt_kv8_accumulate", self._start(start), q.shape[0], max_new, q.shape[1], b,
+                   q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, self._lse(lse, q))
+
+    def _lse(self, lse, q):
+        import torch
+        if lse is None:
+            return None
+        _require(lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous() and
+                 lse.device == self.device, "kv8: lse is float32 [rows, n_head], contiguous, on the cache's device")
+        return lse.data_ptr()
+
+    def evict(self, table_out, budget: int, recent: int, kept):
+        """gpt_kv8_evict: table_out int32 [n_seq, blocks], kept int32 [n_seq, n_head_kv, budget].  Go on with
+        ``cache.table = table_out`` and ``cache.advance(max_new=0, max_len=budget)``."""
+        import torch
+        _require(table_out.dim() == 2 and table_out.shape[0] == self.n_seq and table_out.dtype == torch.int32 and
+                 table_out.is_contiguous() and table_out.device == self.device,
+                 "kv8: table_out is int32 [n_seq, blocks] on the cache's device")
+        _require(kept.dtype == torch.int32 and tuple(kept.shape) == (self.n_seq, self.n_head_kv, budget) and
+                 kept.is_contiguous() and kept.device == self.device, "kv8: kept is int32 [n_seq, n_head_kv, budget]")
+        self._call("kv8_evict", "gpt_kv8_evict", table_out.data_ptr(), table_out.shape[1], budget, recent,
+                   kept.data_ptr())
+
+    def advance(self, start=None, n_rows=None, max_new=1, max_len=0):
+        """gpt_kv8_advance: the lengths grow by the step's rows (n_rows: one for each sequence where None)."""
+        self._call("kv8_advance", "gpt_kv8_advance", self._start(start), self.n_seq if n_rows is None else n_rows,
+                   max_new, max_len)
 
 
 def test_gemm(backend, M, N, K, A, lda, a_kmajor, B, ldb, b_kmajor, epi_kind, act=0, out=None, out2=None, ldo=0,

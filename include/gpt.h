@@ -79,7 +79,11 @@ enum {
   GPT_FLAG_TOKEN_RANGE = 1u << 0,
   GPT_FLAG_NONFINITE_LOSS = 1u << 1,
   GPT_FLAG_NONFINITE_NORM = 1u << 2,
-  GPT_FLAG_TIMEOUT = 1u << 3
+  GPT_FLAG_TIMEOUT = 1u << 3,
+  /* gpt_kv8_* (the cache's own flag word, gpt_kv8_cache.d_flags) */
+  GPT_FLAG_BLOCK_RANGE = 1u << 4, /* a table entry was outside [0, n_blocks): its tokens were left out */
+  GPT_FLAG_CACHE_FULL = 1u << 5,  /* tokens past the table's capacity were not stored                  */
+  GPT_FLAG_ROW_RANGE = 1u << 6    /* offsets were out of order or out of range: a sequence was left out */
 };
 
 /* Plain-old-data model + optimiser configuration.  Field names follow the
@@ -379,6 +383,105 @@ gpt_status gpt_generate(gpt_model* m, const int32_t* d_prompt, int32_t T0, int32
 gpt_status gpt_sample(const void* d_logits, int32_t logits_bf16, int32_t rows, int32_t V, int64_t ld,
                       float temperature, int32_t top_k, float top_p, const float* d_uniform, int32_t* d_out,
                       void* cuda_stream);
+
+/* ---------------------------------------------------------------- 8-bit key / value cache
+ * A cache for decoding many sequences of different lengths (microGPT page,
+ * section "单 GPU 高效推理：采样 + KV Cache", names the cache; the pages give no
+ * format).  Keys and values are e4m3 codes with one scale for each block of
+ * tokens and head: a code c of a block with scale 2^e stands for c 2^e, where
+ * e is the smallest exponent (in [-110, 120]) at which the block's largest
+ * magnitude is at most 448 2^e, e4m3's largest value.
+ *
+ * One step of decoding, for new tokens whose q, k, v rows are at hand:
+ *   gpt_kv8_append      their K and V into slots len .. len + n - 1
+ *   gpt_kv8_attention   new token i (of n) over slots 0 .. len + i
+ *   gpt_kv8_accumulate  (with eviction) adds the attention weights per slot
+ *   gpt_kv8_advance     len += n
+ * None but gpt_kv8_advance changes the lengths, so that the layers of a model
+ * can share one table and one length array (each layer has its own codes,
+ * scales and weights).
+ *
+ * The step's new tokens are the rows of packed arrays: sequence s has rows
+ * d_start[s] .. d_start[s + 1] - 1 (device int32 [n_seq + 1]; at most max_new
+ * rows each, none allowed, n_rows in all arrays); d_start NULL: one row for
+ * each of the first n_rows <= n_seq sequences (max_new 1).  A row's heads are
+ * contiguous, rows ld elements apart; elements are bf16 (rows_bf16) or fp32.
+ * Rows that belong to no sequence are neither read nor written.
+ *
+ * Every call is asynchronous on cuda_stream, allocates nothing and runs on
+ * the current device, which has to be the pointers' and the stream's; calls on
+ * one cache that write it are ordered by the caller.  Host errors come back as
+ * gpt_status; what only the device sees (a block id outside the pool, tokens
+ * past the capacity, bad offsets) is left out, never dereferenced, and sets a
+ * GPT_FLAG_* bit in *d_flags, which the caller clears. */
+typedef struct gpt_kv8_cache {
+  int32_t n_seq;          /* sequences, at most 65535                               */
+  int32_t n_head_kv;      /* key / value heads                                      */
+  int32_t head_dim;       /* 32, 64 or 128 (else GPT_ERR_UNSUPPORTED)               */
+  int32_t block_tokens;   /* tokens a block: 16, 32, 64 or 128                      */
+  int32_t n_blocks;       /* blocks in the pool                                     */
+  int32_t max_blocks;     /* blocks a sequence can have (columns of the table)      */
+  void* d_k;              /* codes [n_blocks, n_head_kv, block_tokens, head_dim],   */
+  void* d_v;              /*   16-byte aligned                                      */
+  float* d_k_scale;       /* [n_blocks, n_head_kv], powers of two                   */
+  float* d_v_scale;
+  float* d_weight;        /* accumulated weights [n_blocks, n_head_kv,
+                             block_tokens]; NULL: no accumulation, no eviction      */
+  const int32_t* d_table; /* [n_seq, max_blocks]: block ids in order                */
+  int32_t* d_len;         /* [n_seq]: tokens held                                   */
+  uint32_t* d_flags;      /* device flag word or NULL                               */
+} gpt_kv8_cache;
+
+/* Quantises the new tokens' keys and values ([n_rows, n_head_kv, head_dim])
+ * into the slots behind the sequences' tokens and sets those slots' weights to
+ * 0.  A block that tokens come into for the first time takes their exponent;
+ * in one that holds earlier tokens the exponent only grows, and where it does
+ * the earlier codes are rounded to the new one (which changes only codes that
+ * become e4m3 subnormals).  Infinities and NaN are stored as NaN, and the
+ * scale goes by the finite values.  A block that two sequences share may be
+ * read by both, but appended to by neither. */
+gpt_status gpt_kv8_append(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
+                          int32_t rows_bf16, const void* d_k, int64_t k_ld, const void* d_v, int64_t v_ld,
+                          void* cuda_stream);
+
+/* Causal attention of the new tokens over the cache: query head h of token i
+ * reads key / value head h / (n_head / n_head_kv), slots 0 .. len + i (the new
+ * tokens' own slots are filled by gpt_kv8_append before).  d_q and d_out
+ * [n_rows, n_head, head_dim]; scale multiplies q k^T.  d_lse (nullable, fp32
+ * [n_rows, n_head]) receives the natural-log sum of the exponentials.  A row
+ * none of whose blocks is in the pool gives zeros and -infinity.  max_len: a
+ * bound on len + n that the caller knows (0: the table's capacity); it decides
+ * how the work is split, not what is read.  fp32 rows are computed to fp32
+ * accuracy (about 1e-6 of the largest value), bf16 rows to fp16's, below bf16's. */
+gpt_status gpt_kv8_attention(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
+                             int32_t n_head, int32_t rows_bf16, const void* d_q, int64_t q_ld, float scale,
+                             int32_t max_len, void* d_out, int64_t out_ld, float* d_lse, void* cuda_stream);
+
+/* Adds to each slot's weight the attention that the new tokens gave it: the sum
+ * of exp(scale q k - lse) over the tokens and over the query heads that read
+ * the key / value head.  Arguments as gpt_kv8_attention's, with its d_lse. */
+gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
+                              int32_t n_head, int32_t rows_bf16, const void* d_q, int64_t q_ld, float scale,
+                              int32_t max_len, const float* d_lse, void* cuda_stream);
+
+/* Eviction by accumulated weight: for every sequence and key / value head,
+ * min(len, budget) slots are kept and moved, in order, into the blocks of
+ * another table (d_table_out [n_seq, max_blocks_out]; the same pool, none of
+ * its blocks in use by any sequence).  Of a sequence over the budget the last
+ * `recent` slots are kept and, of the rest, the budget - recent whose weights
+ * are largest (ties: the lowest slots; NaN below every number).  The heads of
+ * a sequence may keep different slots.  Codes are rounded to their new block's
+ * exponent; weights move along.  d_kept (device int32 [n_seq, n_head_kv,
+ * budget]) receives the kept slots in order, -1 behind the last.  Lengths and
+ * tables stay: the caller goes on with d_table_out and
+ * gpt_kv8_advance(max_new 0, max_len budget). */
+gpt_status gpt_kv8_evict(const gpt_kv8_cache* cache, const int32_t* d_table_out, int32_t max_blocks_out,
+                         int32_t budget, int32_t recent, int32_t* d_kept, void* cuda_stream);
+
+/* len = min(len + n, max_len) for every sequence (max_len 0: the capacity).
+ * max_new 0: n = 0, d_start and n_rows are not used. */
+gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
+                           int32_t max_len, void* cuda_stream);
 
 /* ---------------------------------------------------------------- introspection (tests, resume) */
 

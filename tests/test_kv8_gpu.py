@@ -1,0 +1,484 @@
+"""The 8-bit key / value cache (gpt_kv8_*) against the float64 oracle
+(oracle/kv8.py).
+
+Codes, scales and kept slots are exact: the library divides by powers of two
+and rounds once, as the oracle does.  Attention: both sides read the same codes.
+
+Tolerances, for values v with |v| <= V and rows of weights that sum to 1:
+* bf16 rows.  The weights are rounded to fp16, at most 2^-11 each, and the
+  fp32 sum adds less than 2^-14: |o - o64| <= 2^-10 V before the output's own
+  rounding, 2^-8 |o64|.
+* fp32 rows.  Queries and weights are held to 2^-22 as two fp16 terms.  A
+  score's error is at most 2^-21 of sum |q k| (the terms and the fp32 sum of
+  the MMA, which truncates), and moves a weight by as much relative to it; the
+  base-2 exponential adds 2^-21.  With sum |q k| scale <= B:
+  |o - o64| <= (2 B + 4) 2^-21 V.
+* lse: B 2^-21 + 2^-20 absolute, and its own rounding 2^-23 |lse|; for bf16 rows
+  the same (bf16 queries are exact in fp16, the sum is fp32).
+* accumulated weights: rows * exp() with relative error (2 B + 4) 2^-20 in
+  each term, all of one sign.
+"""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from gpt_decoder_lm_b200 import binding as gb  # noqa: E402
+from oracle import kv8 as O  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def make(seed, lens, H, hd, P, extra=0, weight=True, spread=True, garbage=True):
+    """A cache that holds quantised random tokens, its blocks in random order; what lies behind the sequences'
+    tokens is garbage (NaN codes among it)."""
+    rng = np.random.default_rng(seed)
+    S, cap = len(lens), max(1, -(-(max(lens) + extra) // P))
+    n_blocks = S * cap + 2
+    table = rng.permutation(n_blocks)[:S * cap].reshape(S, cap).astype(np.int32)
+    k = rng.integers(0, 256, (n_blocks, H, P, hd)).astype(np.uint8)
+    v = rng.integers(0, 256, (n_blocks, H, P, hd)).astype(np.uint8)
+    ks = np.exp2(rng.integers(-9, -5, (n_blocks, H)) if spread else np.full((n_blocks, H), -7)).astype(np.float32)
+    vs = np.exp2(rng.integers(-10, -5, (n_blocks, H)) if spread else np.full((n_blocks, H), -7)).astype(np.float32)
+    for s, n in enumerate(lens):  # the tokens' own codes are numbers
+        for j in range(n):
+            b, o = table[s, j // P], j % P
+            for c in (k, v):
+                x = c[b, :, o]
+                x[(x & 127) == 127] ^= 64
+    w = (rng.random((n_blocks, H, P)) ** 4 * 8).astype(np.float32)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    length = np.array(lens, np.int32)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gpu = gb.KV8Cache(t(k), t(v), t(ks), t(vs), t(table), t(length), t(w) if weight else None, flags)
+    return gpu, O.Cache(k, v, ks, vs, table, length, w if weight else None), rng
+
+
+def starts(news):
+    return np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+
+
+def rows_of(rng, n, heads, hd, dtype, wide=True, gain=1.0):
+    """[n, heads, hd] rows, part of wider ones, and the same values in float64."""
+    x = torch.from_numpy(rng.standard_normal((n, heads + (2 if wide else 0), hd)).astype(np.float32) * gain).to(DT[dtype])
+    view = x.cuda()[:, (1 if wide else 0):(1 if wide else 0) + heads]
+    return view, x[:, (1 if wide else 0):(1 if wide else 0) + heads].double().numpy()
+
+
+def same_cache(gpu, ref):
+    assert np.array_equal(gpu.k.cpu().numpy(), ref.k)
+    assert np.array_equal(gpu.v.cpu().numpy(), ref.v)
+    assert np.array_equal(gpu.k_scale.cpu().numpy().astype(np.float64), ref.ks)
+    assert np.array_equal(gpu.v_scale.cpu().numpy().astype(np.float64), ref.vs)
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(a).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,news,H,hd,P", [
+    ([0, 5, 15, 16, 40], [1, 1, 1, 1, 1], 2, 64, 16),
+    ([0, 5, 31, 32, 33], [70, 0, 1, 3, 64], 3, 32, 32),
+    ([7], [300], 1, 128, 128),
+    ([0, 63], [64, 2], 5, 128, 64),
+])
+def test_append_codes(lens, news, H, hd, P, dtype):
+    gpu, ref, rng = make(1, lens, H, hd, P, extra=max(news))
+    st = starts(news)
+    k, k64 = rows_of(rng, int(st[-1]), H, hd, dtype, gain=0.3)
+    v, v64 = rows_of(rng, int(st[-1]), H, hd, dtype)
+    gpu.append(k, v, start=dev(st), max_new=max(news))
+    ref.append(k64, v64, st)
+    same_cache(gpu, ref)
+    assert np.array_equal(gpu.weight.cpu().numpy().astype(np.float64), ref.weight)
+    assert int(gpu.flags) == 0
+    assert gpu.length.tolist() == lens
+
+
+def test_append_one_row_a_sequence_and_unaligned_rows():
+    gpu, ref, rng = make(2, [3, 16, 0, 9], 2, 64, 16, extra=1)
+    base = torch.randn(4 * 2 * 2 * 64 + 3, device="cuda").bfloat16()
+    k = base[1:1 + 4 * 128].reshape(4, 2, 64)          # 2-byte aligned
+    v = base[3:3 + 4 * 129].as_strided((4, 2, 64), (129, 64, 1), 3)  # odd pitch
+    gpu.append(k, v)
+    ref.append(k.double().cpu().numpy(), v.double().cpu().numpy(), starts([1] * 4))
+    same_cache(gpu, ref)
+
+
+def test_append_scale_grows_and_subnormals():
+    """Token by token into one block, each larger than the last: the earlier codes are rounded to the larger scale,
+    down to zero."""
+    gpu, ref, _ = make(3, [0], 1, 32, 16, extra=16)
+    rng = np.random.default_rng(4)
+    for i in range(16):
+        x = (rng.standard_normal((1, 1, 32)) * 2.0 ** (i * 1.5 - 8)).astype(np.float32)
+        gpu.append(torch.from_numpy(x).cuda(), torch.from_numpy(-x).cuda())
+        ref.append(x.astype(np.float64), -x.astype(np.float64), starts([1]))
+        same_cache(gpu, ref)
+        gpu.advance()
+        ref.length += 1
+    assert int(gpu.length) == 16
+
+
+@pytest.mark.parametrize("value", [0.0, 448.0, 449.0, 1e-38, 1e-45, 3e38, 2.0 ** -119, 7.0 * 2.0 ** -120])
+def test_append_extremes(value):
+    gpu, ref, _ = make(5, [0], 1, 32, 16, extra=2)
+    x = np.zeros((2, 1, 32), np.float32)
+    x[0, 0, 3] = value
+    x[1, 0, 4] = -value / 3
+    gpu.append(torch.from_numpy(x).cuda(), torch.from_numpy(x).cuda(), start=dev(starts([2])), max_new=2)
+    ref.append(x.astype(np.float64), x.astype(np.float64), starts([2]))
+    same_cache(gpu, ref)
+
+
+def test_append_not_finite():
+    gpu, _, _ = make(6, [0], 1, 32, 16, extra=4)
+    x = np.ones((4, 1, 32), np.float32)
+    x[1, 0, 5], x[2, 0, 6], x[3, 0, 7] = np.nan, np.inf, -np.inf
+    gpu.append(torch.from_numpy(x).cuda(), torch.from_numpy(x).cuda(), start=dev(starts([4])), max_new=4)
+    b = int(gpu.table[0, 0])
+    got = O.decode(gpu.k.cpu().numpy()[b, 0, :4]) * float(gpu.k_scale[b, 0])
+    bad = ~np.isfinite(x[:, 0])
+    assert np.isnan(got[bad]).all() and (got[~bad] == 1.0).all()
+
+
+def check_attention(gpu, ref, q, q64, st, news, dtype, scale=None, max_len=0, v_max=None, out=None):
+    n, H, hd = q.shape
+    out = torch.full((n, H, hd), 7.0, dtype=DT[dtype], device="cuda") if out is None else out
+    lse = torch.full((n, H), 7.0, device="cuda")
+    gpu.attention(q, out, start=dev(st), max_new=max(max(news), 1), lse=lse, scale=scale, max_len=max_len)
+    sc = hd ** -0.5 if scale is None else scale
+    o64, l64, probs = ref.attention(q64, st, sc)
+    G = H // ref.k.shape[1]
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for s, n_new in enumerate(news):
+        if n_new == 0:
+            continue
+        r = slice(st[s], st[s + 1])
+        kk, there = ref.values(s, int(ref.length[s]) + n_new, "k")
+        vv, _ = ref.values(s, int(ref.length[s]) + n_new, "v")
+        B = max(float(np.max(np.abs(sc) * np.abs(kk[:, h // G]) @ np.abs(q64[r, h]).T)) for h in range(H)) if len(kk) else 0.0
+        V = float(np.abs(vv).max()) if len(vv) else 0.0
+        tol = (2 * B + 4) * 2.0 ** -21 * V
+        tol_o = tol + (2.0 ** -10 * V + 2.0 ** -8 * np.abs(o64[r]) if dtype == "bf16" else 2.0 ** -24 * np.abs(o64[r]))
+        assert (np.abs(got[r] - o64[r]) <= tol_o + 1e-30).all(), (s, np.abs(got[r] - o64[r]).max(), np.min(tol_o))
+        inf = np.isneginf(l64[r])
+        assert np.array_equal(np.isneginf(gl[r]), inf)
+        d = np.abs(gl[r][~inf] - l64[r][~inf])
+        assert (d <= B * 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -23 * np.abs(l64[r])[~inf]).all(), (s, d.max())
+    return out, lse, probs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,P,H,G", [(64, 16, 3, 1), (128, 64, 2, 4), (32, 128, 1, 8), (64, 32, 2, 12), (128, 16, 1, 16),
+                                      (32, 16, 2, 3)])
+def test_attention_one_token(hd, P, H, G, dtype):
+    lens = [0, 1, 15, 16, 31, 47, 130, 700]
+    gpu, ref, rng = make(10, [n + 1 for n in lens], H, hd, P)
+    ref.length -= 1
+    gpu.length -= 1
+    q, q64 = rows_of(rng, len(lens), H * G, hd, dtype)
+    check_attention(gpu, ref, q, q64, starts([1] * len(lens)), [1] * len(lens), dtype)
+    assert int(gpu.flags) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,P,H,G,lens,news", [
+    (64, 16, 2, 1, [0, 3, 40], [1, 17, 33]),
+    (64, 32, 1, 3, [0, 100, 0, 7], [40, 0, 5, 2]),
+    (128, 64, 1, 2, [61, 0], [5, 64]),
+    (32, 128, 2, 5, [0, 300], [3, 2]),
+])
+def test_attention_many_tokens(hd, P, H, G, lens, news, dtype):
+    gpu, ref, rng = make(11, [a + b for a, b in zip(lens, news)], H, hd, P)
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), H * G, hd, dtype)
+    check_attention(gpu, ref, q, q64, st, news, dtype)
+
+
+def test_attention_splits_agree_with_the_oracle():
+    """One sequence, long enough to be split over a cluster's blocks; the bound on the length decides how."""
+    gpu, ref, rng = make(12, [5001], 1, 64, 16)
+    gpu.length -= 1
+    ref.length -= 1
+    q, q64 = rows_of(rng, 1, 2, 64, "fp32")
+    for max_len in (0, 1, 300, 2500, 10 ** 6):
+        check_attention(gpu, ref, q, q64, starts([1]), [1], "fp32", max_len=max_len)
+
+
+def test_attention_scale_ranges():
+    """Blocks whose value scales are far apart, and where the large weight sits on the small values."""
+    gpu, ref, rng = make(13, [64], 1, 64, 16, spread=False)
+    for i, e in enumerate([-60, 20, -7, -30]):
+        b = int(ref.table[0, i])
+        ref.vs[b] = 2.0 ** e
+        gpu.v_scale[b] = 2.0 ** e
+    ref.length -= 1
+    gpu.length -= 1
+    q, q64 = rows_of(rng, 1, 1, 64, "fp32", gain=0.2)
+    check_attention(gpu, ref, q, q64, starts([1]), [1], "fp32")
+    # all weight on the block with scale 2^-60: its values come out to fp32 accuracy of themselves
+    k = ref.k.copy()
+    k[:] = O.encode(np.zeros(k.shape))
+    k[int(ref.table[0, 0]), 0, :, 0] = O.encode(np.array(448.0))
+    ref.k = k
+    gpu.k.copy_(torch.from_numpy(k))
+    q64 = np.zeros((1, 1, 64))
+    q64[0, 0, 0] = 1000.0
+    q = torch.from_numpy(q64.astype(np.float32)).cuda()
+    out = torch.zeros(1, 1, 64, device="cuda")
+    gpu.attention(q, out)
+    o64, _, _ = ref.attention(q64, starts([1]), 0.125)
+    assert np.abs(out.double().cpu().numpy() - o64).max() <= 2.0 ** -19 * 448 * 2.0 ** -60
+
+
+def test_attention_nan_reaches_only_rows_that_see_it():
+    """A NaN in a token's V (and in another's K) makes the rows that see it NaN, in that dimension (or all), and no
+    earlier row."""
+    gpu, ref, rng = make(14, [40], 1, 64, 16)
+    gpu.length.fill_(20)
+    b = int(ref.table[0, 30 // 16])
+    gpu.v[b, 0, 30 % 16, 11] = 0x7F
+    q, _ = rows_of(rng, 20, 1, 64, "bf16")
+    out = torch.zeros(20, 1, 64, dtype=torch.bfloat16, device="cuda")
+    gpu.attention(q, out, start=dev(starts([20])), max_new=20)
+    nan = torch.isnan(out[:, 0]).cpu().numpy()
+    want = np.zeros((20, 64), bool)
+    want[10:, 11] = True
+    assert np.array_equal(nan, want)
+    gpu.k[b, 0, 30 % 16, 5] = 0xFF
+    gpu.attention(q, out, start=dev(starts([20])), max_new=20)
+    nan = torch.isnan(out[:, 0]).cpu().numpy()
+    assert nan[10:].all() and not nan[:10].any()
+
+
+def test_bad_tables_and_offsets_are_left_out():
+    """Block ids outside the pool, offsets out of order and tokens past the capacity: nothing is read or written there,
+    the rest is as ever, and the flag word says so."""
+    gpu, ref, rng = make(15, [33, 20, 16], 2, 64, 16)
+    table = ref.table.copy()
+    table[0, 1], table[1, 0], table[1, 1] = -1, ref.k.shape[0], 2 ** 31 - 1
+    ref.table = table
+    gpu.table = torch.from_numpy(table).cuda()
+    ref.length -= 1
+    gpu.length -= 1
+    q, q64 = rows_of(rng, 3, 2, 64, "fp32")
+    out, lse, probs = check_attention(gpu, ref, q, q64, starts([1] * 3), [1] * 3, "fp32")
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()  # sequence 1 has no block at all
+    assert int(gpu.flags) == gb.FLAG_BLOCK_RANGE
+    gpu.accumulate(q, lse)
+    ref.accumulate(probs)
+    np.testing.assert_allclose(gpu.weight.cpu().numpy(), ref.weight, rtol=1e-4)
+    gpu.append(q, q)
+    ref.append(q64, q64, starts([1] * 3))
+    same_cache(gpu, ref)
+    gpu.flags.zero_()
+    # sequence 1's offsets descend: it has no rows; sequence 0 takes more than max_new
+    before = gpu.k.clone()
+    gpu.append(q, q, start=torch.tensor([0, 3, 2, 3], dtype=torch.int32, device="cuda"), max_new=2)
+    assert int(gpu.flags) == gb.FLAG_ROW_RANGE
+    changed = (gpu.k != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert set(changed) <= {int(table[2, 15 // 16])}
+    gpu.flags.zero_()
+    gpu.length.fill_(48)  # the capacity
+    before = gpu.k.clone()
+    gpu.append(q, q)
+    assert int(gpu.flags) == gb.FLAG_CACHE_FULL and torch.equal(gpu.k, before)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    gpu, ref, rng = make(16, [5, 9], 1, 64, 16)
+    gpu.length.fill_(3)
+    ref.length[:] = 3
+    st = np.array([0, 2, 3], np.int32)
+    q, q64 = rows_of(rng, 6, 1, 64, "bf16")
+    out, lse, _ = check_attention(gpu, ref, q, q64, st, [2, 1], "bf16")
+    assert (out[3:] == 7).all() and (lse[3:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,P,H,G,lens,news", [
+    (64, 16, 3, 1, [0, 1, 33, 600], [1, 1, 1, 1]),
+    (128, 64, 1, 4, [5, 300], [20, 3]),
+    (32, 32, 2, 7, [0, 63, 64], [65, 0, 2]),
+    (64, 128, 1, 20, [129], [1]),
+])
+def test_accumulate(hd, P, H, G, lens, news, dtype):
+    gpu, ref, rng = make(20, [a + b for a, b in zip(lens, news)], H, hd, P)
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), H * G, hd, dtype, gain=0.5)
+    out, lse, probs = check_attention(gpu, ref, q, q64, st, news, dtype)
+    before = gpu.weight.clone().cpu().numpy()
+    gpu.accumulate(q, lse, start=dev(st), max_new=max(news))
+    w0 = ref.weight.copy()
+    ref.accumulate(probs)
+    got = gpu.weight.cpu().numpy().astype(np.float64)
+    B = max(float(np.max(hd ** -0.5 * np.abs(ref.values(s, lens[s] + news[s], "k")[0][:, h // G])
+                         @ np.abs(q64[st[s]:st[s + 1], h]).T, initial=0.0))
+            for s in range(len(lens)) for h in range(H * G))
+    gain = ref.weight - w0
+    assert (np.abs(got - ref.weight) <= (2 * B + 4) * 2.0 ** -20 * gain + 2.0 ** -23 * ref.weight + 1e-30).all()
+    assert np.array_equal(got[gain == 0], before[gain == 0])  # slots that no row sees
+    # each row's weights sum to 1
+    total = sum(n * H * G for n in news)
+    assert abs((got - before).sum() - total) <= 1e-3 * total
+    # again: the same sums, bit for bit
+    gpu2, _, rng2 = make(20, [a + b for a, b in zip(lens, news)], H, hd, P)
+    gpu2.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    gpu2.accumulate(q, lse, start=dev(st), max_new=max(news))
+    assert torch.equal(gpu2.weight, gpu.weight)
+
+
+@pytest.mark.parametrize("H,hd,P,lens,budget,recent", [
+    (2, 64, 16, [100, 30, 31, 64, 0, 1], 31, 7),
+    (1, 128, 64, [1000], 257, 257),
+    (3, 32, 32, [129, 400], 64, 0),
+    (1, 64, 128, [300, 5], 1, 0),
+    (2, 64, 16, [50], 1, 1),
+])
+def test_evict(H, hd, P, lens, budget, recent):
+    gpu, ref, rng = make(30, lens, H, hd, P)
+    S, out_cap = len(lens), -(-budget // P)
+    # a pool with more blocks: those of the table to move into
+    n0 = ref.k.shape[0]
+    grow = lambda a: np.concatenate([a, rng.integers(0, 256, (S * out_cap,) + a.shape[1:]).astype(a.dtype)])  # noqa: E731
+    ref = O.Cache(grow(ref.k), grow(ref.v), np.concatenate([ref.ks, np.ones((S * out_cap, H))]),
+                  np.concatenate([ref.vs, np.ones((S * out_cap, H))]), ref.table, ref.length, grow(ref.weight))
+    ref.weight[:n0][ref.weight[:n0] < 1e-3] = 0.0  # ties
+    ref.weight[int(ref.table[0, 0]), 0, 0] = np.nan
+    t = lambda a, d: torch.from_numpy(np.ascontiguousarray(a.astype(d))).cuda()  # noqa: E731
+    gpu = gb.KV8Cache(t(ref.k, np.uint8), t(ref.v, np.uint8), t(ref.ks, np.float32), t(ref.vs, np.float32),
+                      t(ref.table, np.int32), t(ref.length, np.int32), t(ref.weight, np.float32), gpu.flags)
+    ref.weight = gpu.weight.double().cpu().numpy()
+    table_out = (n0 + rng.permutation(S * out_cap)).reshape(S, out_cap).astype(np.int32)
+    kept = torch.full((S, H, budget), 99, dtype=torch.int32, device="cuda")
+    gpu.evict(dev(table_out), budget, recent, kept)
+    want = ref.evict(table_out, budget, recent)
+    assert np.array_equal(kept.cpu().numpy(), want)
+    same_cache(gpu, ref)
+    assert np.array_equal(gpu.weight.cpu().numpy().astype(np.float64), ref.weight, equal_nan=True)
+    gpu.table = dev(table_out)
+    gpu.advance(max_new=0, max_len=budget)
+    assert gpu.length.tolist() == [min(n, budget) for n in lens]
+    assert int(gpu.flags) == 0
+
+
+def test_evict_ties_keep_the_lowest_slots_and_long_sequences():
+    """Equal weights, and a sequence too long for the selection's shared memory."""
+    for n, budget, recent in ((700, 300, 20), (45000, 900, 100)):
+        H, hd, P = 1, 32, 128
+        cap, out_cap = -(-n // P), -(-budget // P)
+        c = gb.KV8Cache.allocate(1, H, hd, P, cap, n_blocks=cap + out_cap, weight=True)
+        c.length.fill_(n)
+        c.k_scale.fill_(1.0), c.v_scale.fill_(1.0)
+        c.weight.fill_(0.25)
+        heavy = torch.arange(0, n - recent, 50, device="cuda")[:200]
+        c.weight.view(cap + out_cap, P)[heavy // P, heavy % P] = torch.rand(heavy.numel(), device="cuda") + 1.0
+        kept = torch.zeros(1, 1, budget, dtype=torch.int32, device="cuda")
+        c.evict(torch.arange(cap, cap + out_cap, dtype=torch.int32, device="cuda")[None].contiguous(), budget, recent, kept)
+        h = set(heavy.tolist()[:budget - recent])
+        rest = [j for j in range(n - recent) if j not in h][:budget - recent - len(h)]
+        assert kept[0, 0].tolist() == sorted(h | set(rest)) + list(range(n - recent, n))
+
+
+def test_a_run_of_steps_with_eviction():
+    """Append, attention, accumulation, eviction and advance over many steps, as decoding uses them."""
+    rng = np.random.default_rng(40)
+    S, H, G, hd, P, budget, recent, most = 3, 2, 2, 64, 16, 40, 8, 56
+    cap, out_cap = -(-most // P), -(-budget // P)
+    c = gb.KV8Cache.allocate(S, H, hd, P, cap, n_blocks=2 * S * cap, weight=True)
+    tables = [c.table, c.table + S * cap]
+    ref = O.Cache(c.k.cpu().numpy(), c.v.cpu().numpy(), c.k_scale.cpu().numpy(), c.v_scale.cpu().numpy(),
+                  c.table.cpu().numpy(), c.length.cpu().numpy(), c.weight.cpu().numpy())
+    st = starts([21, 3, 1])  # prompts
+    news = [21, 3, 1]
+    kept = torch.zeros(S, H, budget, dtype=torch.int32, device="cuda")
+    for step in range(60):
+        n = int(st[-1])
+        q, q64 = rows_of(rng, n, H * G, hd, "bf16")
+        k, k64 = rows_of(rng, n, H, hd, "bf16")
+        v, v64 = rows_of(rng, n, H, hd, "bf16")
+        c.append(k, v, start=dev(st), max_new=max(news))
+        ref.append(k64, v64, st)
+        same_cache(c, ref)
+        out, lse, probs = check_attention(c, ref, q, q64, st, news, "bf16")
+        c.accumulate(q, lse, start=dev(st), max_new=max(news))
+        ref.accumulate(probs)
+        np.testing.assert_allclose(c.weight.cpu().numpy(), ref.weight, rtol=1e-4, atol=1e-6)
+        ref.weight = c.weight.double().cpu().numpy()  # so that near ties fall alike
+        c.advance(start=dev(st), n_rows=n, max_new=max(news))
+        ref.length = ref.length + np.array(news)
+        if ref.length.max() >= most - 1:
+            tables = tables[::-1]
+            c.evict(tables[0], budget, recent, kept)
+            assert np.array_equal(kept.cpu().numpy(), ref.evict(tables[0].cpu().numpy(), budget, recent))
+            c.table = tables[0]
+            c.advance(max_new=0, max_len=budget)
+            ref.table, ref.length = tables[0].cpu().numpy(), np.minimum(ref.length, budget)
+            same_cache(c, ref)
+        assert c.length.tolist() == ref.length.tolist()
+        st, news = starts([1] * S), [1] * S
+    assert int(c.flags) == 0
+
+
+def test_captured_and_on_another_stream():
+    """A captured step replays on new contents; a step on another stream gives the same bits."""
+    gpu, ref, rng = make(50, [30, 100], 2, 64, 16, extra=4)
+    q, _ = rows_of(rng, 2, 4, 64, "bf16", wide=False)
+    k, _ = rows_of(rng, 2, 2, 64, "bf16", wide=False)
+    out, lse = torch.zeros_like(q), torch.zeros(2, 4, device="cuda")
+
+    def step():
+        gpu.append(k, k)
+        gpu.attention(q, out, lse=lse)
+        gpu.accumulate(q, lse)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(3):
+        k.copy_(torch.randn_like(k))
+        q.copy_(torch.randn_like(q))
+        w = gpu.weight.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), lse.clone(), gpu.weight.clone(), gpu.k.clone()
+        gpu.weight.copy_(w)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        s.synchronize()
+        for a, b in zip(got, (out, lse, gpu.weight, gpu.k)):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes of codes: the last blocks hold the sequence."""
+    hd, P, H = 128, 128, 64
+    per = H * P * hd  # bytes of a block: 1 MiB
+    n_blocks = (1 << 32) // per + 4
+    k = torch.zeros(n_blocks, H, P, hd, dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.full((n_blocks, H), 2.0 ** -7, device="cuda")
+    table = torch.tensor([[n_blocks - 1, n_blocks - 2]], dtype=torch.int32, device="cuda")
+    length = torch.tensor([130], dtype=torch.int32, device="cuda")
+    c = gb.KV8Cache(k, v, ks, ks.clone(), table, length)
+    x = torch.randn(1, H, hd, device="cuda")
+    c.append(x, x)
+    assert int((k[n_blocks - 2, :, 2] != 0).sum()) > H * hd // 2 and int(k[:4].max()) == 0
+    out = torch.zeros(1, H, hd, device="cuda")
+    c.attention(torch.zeros_like(x), out)  # the mean of the values
+    got = (out * 131 - x).abs().max()
+    assert float(got) <= 2.0 ** -3 * float(x.abs().max())  # the codes' rounding, 2^-4 of the value
