@@ -90,6 +90,7 @@ _PROTOS = {
     "gpt_eval_loss": (I32, [P, P, U64, U64, I32, P]),
     "gpt_sample": (I32, [P, I32, I32, I32, I64, F32, I32, F32, P, P, P]),
     "gpt_generate": (I32, [P, P, I32, I32, F32, I32, F32, P, P]),
+    "gpt_sample_rows": (I32, [P, I32, I32, I32, I64, P, P, P, P, P, P, P, P]),
     "gpt_kv8_append": (I32, [P, P, I32, I32, I32, P, I64, P, I64, P]),
     "gpt_kv8_attention": (I32, [P, P, I32, I32, I32, I32, P, I64, F32, I32, P, I64, P, P]),
     "gpt_kv8_accumulate": (I32, [P, P, I32, I32, I32, I32, P, I64, F32, I32, P, P]),
@@ -514,6 +515,36 @@ def sample(logits, temperature: float, top_k: int, top_p: float, uniform, out, V
     st = stream if stream is not None else torch.cuda.current_stream().cuda_stream
     _check(lib().gpt_sample(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, rows, V or ld, ld, temperature,
                             top_k, top_p, _ptr(uniform), _ptr(out), st), None, "sample")
+
+
+def sample_rows(logits, uniform, out, temperature=None, top_k=None, top_p=None, min_p=None, logp=None, V=None):
+    """gpt_sample_rows on the logits' device and its current stream: one draw per row of logits [rows, ld] (bf16 or
+    fp32, contiguous rows).  uniform, temperature, top_p, min_p, logp: float32 [rows]; out, top_k: int32 [rows]."""
+    import torch
+    _require(logits.dim() == 2 and logits.dtype in (torch.bfloat16, torch.float32) and logits.stride(1) == 1,
+             "sample_rows: logits are [rows, ld] of bfloat16 or float32 with contiguous rows")
+    rows, cols = logits.shape
+    V = V or cols
+    ld = max(logits.stride(0), cols) if rows == 1 else logits.stride(0)
+    _require(V <= cols and ld >= cols, "sample_rows: more columns than the logits have, or rows that overlap")
+    ptr = []
+    for t, dtype in ((temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32), (min_p, torch.float32),
+                     (uniform, torch.float32), (out, torch.int32), (logp, torch.float32)):
+        if t is None:
+            ptr.append(None)
+            continue
+        _require(t.dtype == dtype and t.shape == (rows,) and t.is_contiguous() and t.device == logits.device,
+                 "sample_rows: parameters are contiguous [rows] arrays (float32; top_k and out int32) on the logits' device")
+        ptr.append(t.data_ptr())
+    args = (logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, rows, V, ld, *ptr,
+            torch.cuda.current_stream(logits.device).cuda_stream)
+    if torch.cuda.current_device() != logits.device.index:
+        with torch.cuda.device(logits.device):
+            st = lib().gpt_sample_rows(*args)
+    else:
+        st = lib().gpt_sample_rows(*args)
+    if st:
+        _check(st, None, "sample_rows")
 
 
 def _require(cond: bool, msg: str):

@@ -1772,6 +1772,29 @@ gpt_status gpt_sample(const void* d_logits, int32_t logits_bf16, int32_t rows, i
   return cudaGetLastError() == cudaSuccess ? GPT_OK : GPT_ERR_CUDA;
 }
 
+gpt_status gpt_sample_rows(const void* d_logits, int32_t logits_bf16, int32_t rows, int32_t V, int64_t ld,
+                           const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                           const float* d_min_p, const float* d_uniform, int32_t* d_out, float* d_logp,
+                           void* cuda_stream) {
+  if (!d_logits || !d_uniform || !d_out || rows < 1 || V < 1 || ld < V ||
+      (reinterpret_cast<uintptr_t>(d_logits) & (logits_bf16 ? 1 : 3)) != 0)
+    return GPT_ERR_INVALID_ARG;
+  if (V > SAMPLE_MAX_V || rows > 65535) return GPT_ERR_UNSUPPORTED;
+  Ctx c;
+  c.stream = (cudaStream_t)cuda_stream;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GPT_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) c.num_sms = sms;
+  const bool clean_before = cudaPeekAtLastError() == cudaSuccess;  // else: the caller's own, neither reported nor cleared
+  const bool ok = sample_rows_each(c, d_logits, logits_bf16 != 0, rows, V, ld, d_temperature, d_top_k, d_top_p, d_min_p,
+                                   d_uniform, d_out, d_logp);
+  if (clean_before && cudaPeekAtLastError() != cudaSuccess) {
+    cudaGetLastError();
+    return GPT_ERR_CUDA;
+  }
+  return ok ? GPT_OK : GPT_ERR_CUDA;
+}
+
 gpt_status gpt_gather_batch(gpt_model* m, const void* d_stream, uint64_t stream_len, uint64_t data_seed, int32_t step,
                             int32_t micro, int32_t* d_idx, int32_t* d_tgt) {
   if (!m || !d_stream || !d_idx || !d_tgt) return fail(m, GPT_ERR_INVALID_ARG, "gather_batch: null argument");

@@ -262,5 +262,11 @@ void dropout_mask(Ctx& c, DropKey k, long n, uint8_t* out);
 // one draw per row of logits [rows, ld] (temperature, top-k, top-p, uniform[row])
 void sample_rows(Ctx& c, const void* logits, bool bf16_logits, int rows, int V, long ld, float temperature, int top_k,
                  float top_p, const float* uniform, int32_t* out);
+// the same with parameters per row (each array may be null: off) and min-p; logp (nullable): the drawn token's
+// log-probability.  V at most SAMPLE_MAX_V (token weights are summed as 64-bit integers).  False: launch failed
+constexpr int SAMPLE_MAX_V = 1 << 19;
+bool sample_rows_each(Ctx& c, const void* logits, bool bf16_logits, int rows, int V, long ld, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, int32_t* out,
+                      float* logp);
 
 }  // namespace gpt

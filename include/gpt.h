@@ -384,6 +384,28 @@ gpt_status gpt_sample(const void* d_logits, int32_t logits_bf16, int32_t rows, i
                       float temperature, int32_t top_k, float top_p, const float* d_uniform, int32_t* d_out,
                       void* cuda_stream);
 
+/* gpt_sample with parameters for each row, and min-p.  d_temperature,
+ * d_top_k, d_top_p, d_min_p: device arrays [rows], each nullable (1, off, off,
+ * off).  For a row, in this order:
+ *   temperature not > 0   greedy: the arg-max, lowest index on ties
+ *   0 < top_k < V         keeps the logits >= the k-th largest (ties kept)
+ *   top_p < 1             of those, keeps p >= tau for the largest tau whose
+ *                         kept mass reaches top_p of theirs (<= 0: the maximum)
+ *   min_p > 0             of those, keeps p >= min_p * the largest p (> 1: 1)
+ * with p = exp((z - max) / temperature), and the token is the first, in index
+ * order, whose running kept mass exceeds d_uniform[row] (in [0, 1)) times the
+ * kept mass.  A logit that is -infinity or NaN is never drawn; +infinity shares
+ * the row with its equals; a row with nothing to draw from gives -1.  d_logp
+ * (nullable, fp32 [rows]): the natural log of the drawn token's probability
+ * among the kept ones (0 for greedy rows, -infinity with token -1).
+ * Probabilities and their sums are held to about 2^-34 (gpt_sample's to fp32),
+ * so that the result does not depend on how a row is divided over the GPU.
+ * rows <= 65535, V <= 524288.  Asynchronous on cuda_stream. */
+gpt_status gpt_sample_rows(const void* d_logits, int32_t logits_bf16, int32_t rows, int32_t V, int64_t ld,
+                           const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                           const float* d_min_p, const float* d_uniform, int32_t* d_out, float* d_logp,
+                           void* cuda_stream);
+
 /* ---------------------------------------------------------------- 8-bit key / value cache
  * A cache for decoding many sequences of different lengths (microGPT page,
  * section "单 GPU 高效推理：采样 + KV Cache", names the cache; the pages give no

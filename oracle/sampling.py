@@ -41,7 +41,7 @@ import numpy as np
 
 from . import gpt_oracle as go
 
-__all__ = ["eval_loss", "sample_row", "sample_rows", "generate"]
+__all__ = ["eval_loss", "sample_row", "sample_rows", "sample_row_minp", "generate"]
 
 
 def eval_loss(cfg: go.Config, P: Dict[str, np.ndarray], stream: np.ndarray, data_seed: int, n_batches: int) -> float:
@@ -94,6 +94,33 @@ def sample_row(z: np.ndarray, temperature: float, top_k: int, top_p: float, u: f
 def sample_rows(Z: np.ndarray, temperature: float, top_k: int, top_p: float, U: np.ndarray) -> np.ndarray:
     return np.array([sample_row(Z[r], temperature, top_k, top_p, float(U[r])) for r in range(Z.shape[0])],
                     dtype=np.int64)
+
+
+def sample_row_minp(z: np.ndarray, temperature: float, top_k: int, top_p: float, min_p: float, u: float):
+    """(token, log-probability) of one draw with min_p as well: of the tokens that top_k and top_p keep, those with
+    p >= min_p times the largest p.  -inf and NaN are never drawn, +inf shares the row with its equals; (-1, -inf)
+    where nothing is left, log-probability 0 for a greedy draw."""
+    z = np.where(np.isnan(z), -np.inf, np.asarray(z, dtype=np.float64))
+    zmax = z.max()
+    if zmax == -np.inf:
+        return -1, -np.inf
+    if not temperature > 0:
+        return int(np.argmax(z)), 0.0
+    with np.errstate(invalid="ignore"):
+        p = np.where(z == zmax, 1.0, np.where(np.isfinite(z), np.exp((z - zmax) / temperature), 0.0))
+    if 0 < top_k < len(z):
+        p = np.where(z >= np.sort(z)[len(z) - top_k], p, 0.0)
+    if top_p < 1:
+        order = np.argsort(-z, kind="stable")
+        cum = np.cumsum(p[order])
+        n = min(int(np.searchsorted(cum, max(top_p, 0.0) * cum[-1], side="left")), len(z) - 1)
+        p = np.where(z >= z[order][n], p, 0.0)
+    p = np.where(p >= min(max(min_p, 0.0), 1.0), p, 0.0)
+    c = np.cumsum(p)
+    i = int(np.searchsorted(c, max(u, 0.0) * c[-1], side="right"))
+    if i >= len(c):
+        i = int(np.nonzero(p)[0][-1])
+    return i, float(np.log(p[i] / c[-1]))
 
 
 def generate(cfg: go.Config, P: Dict[str, np.ndarray], prompt: np.ndarray, n_new: int, temperature: float,

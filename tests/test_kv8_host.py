@@ -93,3 +93,12 @@ def test_oracle_codes_are_e4m3():
     assert np.array_equal(O.encode(x), want)
     for a, e in ((448.0, 0), (448.1, 1), (1.75, -8), (1.76, -7), (0.0, O.E_MIN), (1e-38, O.E_MIN), (3e38, 120)):
         assert O.exponent(a) == e
+
+
+def test_sample_rows_refusals(lib):
+    def call(z=A, bf16=1, rows=2, V=10, ld=10, u=A, out=A):
+        return gb.STATUS[lib.gpt_sample_rows(z, bf16, rows, V, ld, None, None, None, None, u, out, None, None)]
+    for kw in (dict(z=None), dict(z=A + 1), dict(z=A + 2, bf16=0), dict(rows=0), dict(V=0), dict(ld=9), dict(u=None),
+               dict(out=None)):
+        assert call(**kw) == "GPT_ERR_INVALID_ARG", kw
+    assert call(V=524289, ld=524289) == "GPT_ERR_UNSUPPORTED" and call(rows=65536) == "GPT_ERR_UNSUPPORTED"
