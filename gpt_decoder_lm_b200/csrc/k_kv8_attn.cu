@@ -5,16 +5,21 @@
 //
 // Row r = (new token i, query head) of a sequence with len tokens before this
 // step sees slots 0 .. len + i.  With G query heads to a key / value head, the
-// n G rows that share one are taken 16 at a time as the 16 rows of the
-// 16 x 8 x 16 warp MMA: each cached byte is read once for all of them.  Codes
+// n G rows that share one are taken 8 NT at a time, as the columns of
+//   S^T = K Q^T   and   O^T = V^T P^T
+// by the 16 x 8 x 16 warp MMA: the cache is on its 16-row side, so that one row
+// of queries (decoding) wastes seven of eight columns and not fifteen of
+// sixteen rows, and a code that has been converted serves NT products.  Codes
 // become fp16 by one exact conversion for two of them; the MMA takes the
-// multiply-adds, so that at one row (most of the MMA empty) as at sixteen the
-// kernel is bound by reading the cache.
+// multiply-adds, so that the kernel is bound by reading the cache, or by the
+// conversions, whatever the number of rows.
 //
 // The order of a dot product's terms and of a sum's is free, which the operand
-// layouts use: lane (g, t) of the QK product takes a contiguous quarter of key
-// g's row, and lane (g, t) of the PV product a contiguous eighth of the rows of
-// four tokens; neither needs a transposition.
+// layouts use: lane (g, t) of the QK product takes a contiguous quarter of two
+// keys' rows, and lane (g, t) of the PV product a contiguous eighth of the rows
+// of four tokens; neither needs a transposition in memory.  P^T, the second
+// product's other operand, is S^T's registers with each 8 x 8 part transposed
+// (movmatrix).
 #include <cooperative_groups.h>
 
 #include "kv8.cuh"
@@ -53,16 +58,23 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows of q as the A operand of the QK product.  bf16 rows are exact in fp16
-// once a power of two has brought the row's largest magnitude to 2^14 .. 2^15
-// (what falls below fp16's range then is under 2^-38 of it); fp32 rows take two
-// fp16 terms, 22 bits, which leaves less than the fp32 sum of the products does.
-template <typename T, int HD, bool R8>
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Rows of q as the B operand of the QK product, 8 NT of them.  bf16 rows are
+// exact in fp16 once a power of two has brought the row's largest magnitude to
+// 2^14 .. 2^15 (what falls below fp16's range then is under 2^-38 of it); fp32
+// rows take two fp16 terms, 22 bits, which leaves less than the fp32 sum of the
+// products does.
+template <typename T, int HD, int NT>
 struct QFrag {
   static constexpr int KS = HD / 16;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
-  uint32_t a[TERMS][KS][R8 ? 2 : 4];
-  float f0, f1;  // of rows g and g + 8: what a score has to be multiplied by to be scale * q k * log2(e)
+  uint32_t b[TERMS][NT][KS][2];
+  float f[NT][2];  // of rows 8 nt + 2 t + e: what a score has to be multiplied by to be scale * q k * log2(e)
 
   // first dimension of the four codes that lane t feeds to step ks
   static __device__ __forceinline__ int dim0(int t, int ks) {
@@ -70,54 +82,69 @@ struct QFrag {
     return (ks / 4) * 64 + t * 16 + (ks % 4) * 4;
   }
 
-  __device__ void load(const T* __restrict__ q, long q_ld, int hd_row, int G, int row0, int R, float scale) {
-    // row r: token r / G, head r % G; hd_row: first element of the group's heads in a row of q
+  // row r: token r / G, head r % G; q: the sequence's first row, at the group's first head
+  __device__ void load(const T* __restrict__ q, long q_ld, int G, int row0, int R, float scale) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const bool vec = ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(q_ld * (long)sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
 #pragma unroll
-    for (int half = 0; half < (R8 ? 1 : 2); half++) {
-      const int r = row0 + g + 8 * half;
+    for (int nt = 0; nt < NT; nt++) {
+      const int r = row0 + 8 * nt + g;
       const bool on = r < R;
-      const T* p = q + (on ? (long)(r / G) * q_ld + hd_row + (r % G) * HD : 0);
+      const T* p = q + (on ? (long)(r / G) * q_ld + (r % G) * HD : 0);
       float x[KS][4];
       float top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ks++)
+      for (int ks = 0; ks < KS; ks++) {
+        T y[4] = {from_f<T>(0.f), from_f<T>(0.f), from_f<T>(0.f), from_f<T>(0.f)};
+        if (on) {
+          const T* e = p + dim0(t, ks);
+          if (vec) {
+            if (sizeof(T) == 2)
+              *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(e);
+            else
+              *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(e);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) y[j] = e[j];
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          x[ks][j] = on ? to_f<T>(p[dim0(t, ks) + j]) : 0.f;
+          x[ks][j] = to_f<T>(y[j]);
           top = fmaxf(top, fabsf(x[ks][j]));
         }
+      }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
       e = min(max(e, -100), 100);
-      const float f = kv8_pow2(e);
-      (half ? f1 : f0) = kv8_pow2(-e) * scale * 1.4426950408889634f;
+      const float up = kv8_pow2(e), down = kv8_pow2(-e) * scale * 1.4426950408889634f;
+      f[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+      f[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
       for (int ks = 0; ks < KS; ks++)
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const float lo = x[ks][2 * j] * f, hi = x[ks][2 * j + 1] * f;
+          const float lo = x[ks][2 * j] * up, hi = x[ks][2 * j + 1] * up;
           const uint32_t v = pack_f16(lo, hi);
-          a[0][ks][R8 ? j : 2 * j + half] = v;
-          if (TERMS == 2) a[TERMS - 1][ks][R8 ? j : 2 * j + half] = pack_rest(lo, hi, v);
+          b[0][nt][ks][j] = v;
+          if (TERMS == 2) b[TERMS - 1][nt][ks][j] = pack_rest(lo, hi, v);
         }
     }
-    if (R8) f1 = 0.f;
   }
 
-  // d += q k^T for eight keys; w: the lane's quarter of its key's codes
-  __device__ __forceinline__ void qk(float (&d)[4], const uint32_t (&w)[KS]) const {
+  // d = k q^T for 16 keys; w0, w1: the lane's quarters of its two keys' codes
+  __device__ __forceinline__ void qk(float (&d)[NT][4], const uint32_t (&w0)[KS], const uint32_t (&w1)[KS]) const {
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ks++) {
-      const uint32_t b0 = f16x2_e4m3(w[ks]), b1 = f16x2_e4m3(w[ks] >> 16);
+      const uint32_t a0 = f16x2_e4m3(w0[ks]), a1 = f16x2_e4m3(w1[ks]);
+      const uint32_t a2 = f16x2_e4m3(w0[ks] >> 16), a3 = f16x2_e4m3(w1[ks] >> 16);
 #pragma unroll
-      for (int m = 0; m < TERMS; m++) {
-        if (R8)
-          mma(d, a[m][ks][0], 0u, a[m][ks][1], 0u, b0, b1);
-        else
-          mma(d, a[m][ks][0], a[m][ks][1], a[m][ks][R8 ? 0 : 2], a[m][ks][R8 ? 0 : 3], b0, b1);
-      }
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int m = 0; m < TERMS; m++) mma(d[nt], a0, a1, a2, a3, b[m][nt][ks][0], b[m][nt][ks][1]);
     }
   }
 };
@@ -136,12 +163,10 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return line * 128 + ((c ^ x) << 4);
 }
 
-// The token, within its 16, of column 2 t + e of the group's n-tile nt: lane t
-// then owns tokens t, t + 4, t + 8, t + 12, in the order that the PV product's
-// operands need them.
-__device__ __forceinline__ int col_token(int t, int nt, int e) { return t + 4 * (e + 2 * nt); }
-// ... and the token of key column g of n-tile nt
-__device__ __forceinline__ int key_token(int g, int nt) { return (g >> 1) + 4 * ((g & 1) + 2 * nt); }
+// The token, within its 16, of the QK product's row g + 8 half.  Lane t of the
+// PV product then owns tokens t, t + 4, t + 8, t + 12 (k = 2 t, 2 t + 1, 2 t + 8,
+// 2 t + 9 of its 16).
+__device__ __forceinline__ int key_token(int g, int half) { return (g >> 1) + 4 * ((g & 1) + 2 * half); }
 
 template <int HD>
 struct alignas(16) Stage {
@@ -162,17 +187,17 @@ struct AttnArgs {
   float* lse;
 };
 
-// One thread block (NW warps): 16 rows (8 with R8) of one key / value head of
-// one sequence, over one of the cluster's equal parts of the slots.  Each warp
-// takes every NW-th tile of 32 tokens through its own ring of NS stages
-// (cp.async, no block-wide barrier in the loop) with its own running maxima and
-// sums; the warps, then the cluster's blocks through distributed shared memory,
-// are joined at the end in a fixed order.
-template <typename T, int HD, bool R8, int NW, int NS>
-__global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
-  constexpr int ROWS = R8 ? 8 : 16;
-  constexpr int NH = R8 ? 1 : 2;      // row halves a lane holds
+// One thread block (NW warps): 8 NT rows of one key / value head of one
+// sequence, over one of the cluster's equal parts of the slots.  Each warp takes
+// every NW-th tile of 32 tokens through its own ring of NS stages (cp.async, no
+// block-wide barrier in the loop) with its own running maxima and sums; the
+// warps, then the cluster's blocks through distributed shared memory, are joined
+// at the end in a fixed order.
+template <typename T, int HD, int NT, int NW, int NS, int MINB>
+__global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs at) {
+  constexpr int ROWS = 8 * NT;
   constexpr int BPL = HD / 8;         // dimensions a lane loads of a V row
+  constexpr int MT = HD / 16;         // 16-dimension tiles of the output
   constexpr int OP = HD + 4;          // pitch of a row of partial outputs
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float st_m[NW][ROWS], st_mv[NW][ROWS], st_l[NW][ROWS];
@@ -186,21 +211,25 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
   const int R = n * G, row0 = rt * ROWS;
   if (row0 >= R) return;  // the same for every block of the cluster
   const int cap = a.max_blocks << a.lgP;
-  const int i_lo = row0 / G, i_hi = min(R - 1, row0 + ROWS - 1) / G;
-  const int see_lo = min(len + i_lo + 1, cap), see_hi = min(len + i_hi + 1, cap);
-  // visible slots of rows g and g + 8
-  const int see[2] = {min(len + min(row0 + g, R - 1) / G + 1, cap), min(len + min(row0 + g + 8, R - 1) / G + 1, cap)};
+  const int see_lo = min(len + row0 / G + 1, cap), see_hi = min(len + min(R - 1, row0 + ROWS - 1) / G + 1, cap);
 
-  QFrag<T, HD, R8> q;
-  q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld, at.q_ld, h * G * HD, G, row0, R, at.scale);
-
-  float o[BPL][4];
+  float o[MT][NT][4];
 #pragma unroll
-  for (int j = 0; j < BPL; j++)
+  for (int i = 0; i < MT; i++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) o[j][i] = 0.f;
-  // per row: running maximum of the scores (log2), that of scores + log2(V scale), and the sum of 2^(score - m)
-  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int nt = 0; nt < NT; nt++) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+  // of rows 8 nt + 2 t + e: running maximum of the scores (log2), that of scores + log2(V scale), the sum of
+  // 2^(score - m), and the slots that the row sees
+  float m[NT][2], mv[NT][2], l[NT][2];
+  int see[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      m[nt][e] = mv[nt][e] = -INFINITY;
+      l[nt][e] = 0.f;
+      see[nt][e] = min(len + min(row0 + 8 * nt + 2 * t + e, R - 1) / G + 1, cap);
+    }
 
   const int tiles = (see_hi + TT - 1) / TT;
   const int per = (tiles + n_split - 1) / n_split;
@@ -217,23 +246,36 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
       b1 = tile * TT + 16 < see_hi ? (j1 == (tile * TT) >> a.lgP ? b0 : kv8_block(a, s, j1)) : -1;
     }
   };
+  // A group's 16 rows are contiguous in its block: chunk u of a tile lies 512 u bytes on, in memory and (but for
+  // the lane's constant) in the stage.
+  constexpr int CPR = HD / 16;
+  const uint32_t to_even = tile_at<HD>(lane / CPR, lane % CPR);
+  const uint32_t to_odd = HD == 128 ? tile_at<HD>(32 / CPR + lane / CPR, lane % CPR) - 512 : to_even;
   auto request = [&](int tile, int slot) {
     if (tile < t1) {
       Stage<HD>& st = ring[slot];
       const int base = tile * TT;
       const size_t p0 = ((size_t)max(b0, 0) * a.H + h), p1 = ((size_t)max(b1, 0) * a.H + h);
+      const size_t s0 = ((p0 << a.lgP) + (base & (a.P - 1))) * HD + lane * 16;
+      const size_t s1 = ((p1 << a.lgP) + ((base + 16) & (a.P - 1))) * HD + lane * 16;
       const uint32_t sk = (uint32_t)__cvta_generic_to_shared(st.k), sv = (uint32_t)__cvta_generic_to_shared(st.v);
-      constexpr int CPR = HD / 16;
+      if (base + TT <= see_hi && b0 >= 0 && b1 >= 0) {
 #pragma unroll
-      for (int u = 0; u < CPR; u++) {
-        const int idx = u * 32 + lane, row = idx / CPR, ch = idx % CPR;
-        const int j = base + row;
-        const bool second = row >= 16;
-        const bool on = j < see_hi && (second ? b1 : b0) >= 0;
-        const size_t src = on ? ((second ? p1 : p0) * a.P + (j & (a.P - 1))) * HD + ch * 16 : 0;
-        const uint32_t dst = tile_at<HD>(row, ch);
-        cp16(sk + dst, a.k + src, on);
-        cp16(sv + dst, a.v + src, on);
+        for (int u = 0; u < CPR; u++) {
+          const size_t src = u < CPR / 2 ? s0 + u * 512 : s1 + (u - CPR / 2) * 512;
+          const uint32_t dst = u * 512 + (u & 1 ? to_odd : to_even);
+          cp16(sk + dst, a.k + src, true);
+          cp16(sv + dst, a.v + src, true);
+        }
+      } else {  // slots that no row sees, and groups without a block, are filled with zeros
+#pragma unroll
+        for (int u = 0; u < CPR; u++) {
+          const bool on = base + (u * 32 + lane) / CPR < see_hi && (u < CPR / 2 ? b0 : b1) >= 0;
+          const size_t src = on ? (u < CPR / 2 ? s0 + u * 512 : s1 + (u - CPR / 2) * 512) : 0;
+          const uint32_t dst = u * 512 + (u & 1 ? to_odd : to_even);
+          cp16(sk + dst, a.k + src, on);
+          cp16(sv + dst, a.v + src, on);
+        }
       }
       if (lane < 4) {
         const size_t p = (lane & 1) ? p1 : p0;
@@ -253,6 +295,8 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
     next += NW;
     look(next);
   }
+  QFrag<T, HD, NT> q;
+  q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, row0, R, at.scale);
   int slot = 0;
   for (int tile = t0 + w; tile < t1; tile += NW) {
     cp_wait<NS - 2>();
@@ -263,94 +307,104 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
     const Stage<HD>& st = ring[slot];
     slot = slot == NS - 1 ? 0 : slot + 1;
 
-    // ---- scores of 4 x 8 keys
-    float sc[4][4];
+    // ---- scores of 2 x 16 keys: [group][rows][key half, row parity]
+    float sc[2][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < 4; nt++) {
-      const int row = (nt >> 1) * 16 + key_token(g, nt & 1);
-      uint32_t kw[HD / 16];
-      if (HD == 32) {
-        const uint2 x = *reinterpret_cast<const uint2*>(st.k + tile_at<HD>(row, t >> 1) + (t & 1) * 8);
-        kw[0] = x.x, kw[1] = x.y;
-      } else {
+    for (int gr = 0; gr < 2; gr++) {
+      uint32_t kw[2][HD / 16];
 #pragma unroll
-        for (int c = 0; c < HD / 64; c++) {
-          const uint4 x = *reinterpret_cast<const uint4*>(st.k + tile_at<HD>(row, c * 4 + t));
-          kw[(4 * c) % (HD / 16)] = x.x, kw[(4 * c + 1) % (HD / 16)] = x.y;
-          kw[(4 * c + 2) % (HD / 16)] = x.z, kw[(4 * c + 3) % (HD / 16)] = x.w;
+      for (int half = 0; half < 2; half++) {
+        const int row = gr * 16 + key_token(g, half);
+        if (HD == 32) {
+          const uint2 x = *reinterpret_cast<const uint2*>(st.k + tile_at<HD>(row, t >> 1) + (t & 1) * 8);
+          kw[half][0] = x.x, kw[half][1] = x.y;
+        } else {
+#pragma unroll
+          for (int c = 0; c < HD / 64; c++) {
+            const uint4 x = *reinterpret_cast<const uint4*>(st.k + tile_at<HD>(row, c * 4 + t));
+            kw[half][(4 * c) % CPR] = x.x, kw[half][(4 * c + 1) % CPR] = x.y;
+            kw[half][(4 * c + 2) % CPR] = x.z, kw[half][(4 * c + 3) % CPR] = x.w;
+          }
         }
       }
-      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-      q.qk(sc[nt], kw);
+      q.qk(sc[gr], kw[0], kw[1]);
     }
     const int ok = st.ok;
     const bool full = tile * TT + TT <= see_lo && ok == 3;
     const float k0 = st.ks[0], k1 = st.ks[1];
     // log2 of the V scales; a group without tokens has none
     const float v0 = ok & 1 ? __log2f(st.vs[0]) : -INFINITY, v1 = ok & 2 ? __log2f(st.vs[1]) : -INFINITY;
-    float top[2] = {-INFINITY, -INFINITY}, topv[2];  // largest score, and score + log2 V scale
-#pragma unroll
-    for (int hf = 0; hf < NH; hf++) {
-      float top0 = -INFINITY;  // of the first group
-      const float f = hf ? q.f1 : q.f0;
-#pragma unroll
-      for (int nt = 0; nt < 4; nt++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          float& x = sc[nt][2 * hf + e];
-          x *= f * (nt < 2 ? k0 : k1);
-          if (!full) {
-            const int j = tile * TT + (nt >> 1) * 16 + col_token(t, nt & 1, e);
-            if (j >= see[hf] || !(ok >> (nt >> 1) & 1)) x = -INFINITY;
-          }
-          if (nt < 2) top0 = fmaxf(top0, x); else top[hf] = fmaxf(top[hf], x);
-        }
-      topv[hf] = fmaxf(top0 + v0, top[hf] + v1);
-      top[hf] = fmaxf(top[hf], top0);
-      top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 1));
-      top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 2));
-      if (v0 == v1) {
-        topv[hf] = top[hf] + v0;
-      } else {
-        topv[hf] = fmaxf(topv[hf], __shfl_xor_sync(0xffffffffu, topv[hf], 1));
-        topv[hf] = fmaxf(topv[hf], __shfl_xor_sync(0xffffffffu, topv[hf], 2));
-      }
-    }
     bool grow = false;
+    float top[NT][2], topv[NT][2];  // largest score, and score + log2 V scale
 #pragma unroll
-    for (int hf = 0; hf < NH; hf++) grow |= top[hf] > m[hf] + LAZY || topv[hf] > mv[hf] + LAZY;
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        float big[2];
+#pragma unroll
+        for (int gr = 0; gr < 2; gr++) {
+          const float f = q.f[nt][e] * (gr ? k1 : k0);
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            float& x = sc[gr][nt][2 * half + e];
+            x *= f;
+            if (!full && (tile * TT + gr * 16 + key_token(g, half) >= see[nt][e] || !(ok >> gr & 1))) x = -INFINITY;
+          }
+          big[gr] = fmaxf(sc[gr][nt][e], sc[gr][nt][2 + e]);
+        }
+        float x = fmaxf(big[0], big[1]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        float y = x + v0;
+        if (v0 != v1) {
+          y = fmaxf(big[0] + v0, big[1] + v1);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+        }
+        top[nt][e] = x;
+        topv[nt][e] = y;
+        grow |= x > m[nt][e] + LAZY || y > mv[nt][e] + LAZY;
+      }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int hf = 0; hf < NH; hf++) {
-        const float m1 = fmaxf(m[hf], top[hf]), mv1 = fmaxf(mv[hf], topv[hf]);
-        const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[hf] - m1), fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[hf] - mv1);
-        m[hf] = m1, mv[hf] = mv1;
-        l[hf] *= fl;
+      for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int j = 0; j < BPL; j++) o[j][2 * hf] *= fo, o[j][2 * hf + 1] *= fo;
-      }
+        for (int e = 0; e < 2; e++) {
+          const float m1 = fmaxf(m[nt][e], top[nt][e]), mv1 = fmaxf(mv[nt][e], topv[nt][e]);
+          const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[nt][e] - m1);
+          const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[nt][e] - mv1);
+          m[nt][e] = m1, mv[nt][e] = mv1;
+          l[nt][e] *= fl;
+#pragma unroll
+          for (int i = 0; i < MT; i++) o[i][nt][e] *= fo, o[i][nt][2 + e] *= fo;
+        }
     }
     // ---- weights: 2^(score - m) for the sum, times 2^(log2 V scale + m - mv) for the product with V's codes
-    uint32_t p[2][4], plo[2][4];
+    uint32_t p[2][NT][2], plo[2][NT][2];
 #pragma unroll
-    for (int hf = 0; hf < NH; hf++) {
-      const float mm = m[hf] == -INFINITY ? 0.f : m[hf], mmv = mv[hf] == -INFINITY ? 0.f : mv[hf];
-      const float c0 = sfu_exp2(v0 + mm - mmv), c1 = sfu_exp2(v1 + mm - mmv);
+    for (int nt = 0; nt < NT; nt++) {
+      float c[2][2];  // [group][row]
+      float mm[2];
 #pragma unroll
-      for (int nt = 0; nt < 4; nt++) {
-        const float x = sfu_exp2(sc[nt][2 * hf] - mm), y = sfu_exp2(sc[nt][2 * hf + 1] - mm);
-        l[hf] += x + y;
-        const float c = nt < 2 ? c0 : c1;
-        const uint32_t v = pack_f16(x * c, y * c);
-        p[nt >> 1][2 * (nt & 1) + hf] = v;
-        if (sizeof(T) == 4) plo[nt >> 1][2 * (nt & 1) + hf] = pack_rest(x * c, y * c, v);
+      for (int e = 0; e < 2; e++) {
+        mm[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+        const float d = mm[e] - (mv[nt][e] == -INFINITY ? 0.f : mv[nt][e]);
+        c[0][e] = sfu_exp2(v0 + d);
+        c[1][e] = v0 == v1 ? c[0][e] : sfu_exp2(v1 + d);
       }
-    }
-    if (R8) {
 #pragma unroll
-      for (int gr = 0; gr < 2; gr++) p[gr][1] = p[gr][3] = plo[gr][1] = plo[gr][3] = 0u;
+      for (int gr = 0; gr < 2; gr++)
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          const float x = sfu_exp2(sc[gr][nt][2 * half] - mm[0]), y = sfu_exp2(sc[gr][nt][2 * half + 1] - mm[1]);
+          l[nt][0] += x;
+          l[nt][1] += y;
+          const uint32_t v = pack_f16(x * c[gr][0], y * c[gr][1]);
+          p[gr][nt][half] = transpose8(v);
+          if (sizeof(T) == 4) plo[gr][nt][half] = transpose8(pack_rest(x * c[gr][0], y * c[gr][1], v));
+        }
     }
-    // ---- o += p v
+    // ---- o += v^T p^T
     bool poison = false;
 #pragma unroll
     for (int gr = 0; gr < 2; gr++) {
@@ -382,33 +436,34 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
       }
 #pragma unroll
       for (int c = 0; c < HD / 32; c++) {
+        // bytes j and j + 1 (x), j + 2 and j + 3 (y) of the tokens' pairs
         const uint32_t x01 = __byte_perm(vw[0][c], vw[1][c], 0x5140), y01 = __byte_perm(vw[0][c], vw[1][c], 0x7362);
         const uint32_t x23 = __byte_perm(vw[2][c], vw[3][c], 0x5140), y23 = __byte_perm(vw[2][c], vw[3][c], 0x7362);
-        const uint32_t bb[4][2] = {{f16x2_e4m3(x01), f16x2_e4m3(x23)},
-                                   {f16x2_e4m3(x01 >> 16), f16x2_e4m3(x23 >> 16)},
-                                   {f16x2_e4m3(y01), f16x2_e4m3(y23)},
-                                   {f16x2_e4m3(y01 >> 16), f16x2_e4m3(y23 >> 16)}};
+        const uint32_t aa[2][4] = {
+            {f16x2_e4m3(x01), f16x2_e4m3(x01 >> 16), f16x2_e4m3(x23), f16x2_e4m3(x23 >> 16)},
+            {f16x2_e4m3(y01), f16x2_e4m3(y01 >> 16), f16x2_e4m3(y23), f16x2_e4m3(y23 >> 16)}};
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          mma(o[4 * c + j], p[gr][0], p[gr][1], p[gr][2], p[gr][3], bb[j][0], bb[j][1]);
-          if (sizeof(T) == 4)  // fp32 outputs: the weights' second fp16 term
-            mma(o[4 * c + j], plo[gr][0], plo[gr][1], plo[gr][2], plo[gr][3], bb[j][0], bb[j][1]);
-        }
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
+            if (sizeof(T) == 4)  // fp32 outputs: the weights' second fp16 term
+              mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], plo[gr][nt][0], plo[gr][nt][1]);
+          }
       }
     }
     if (__any_sync(0xffffffffu, poison)) {
       for (int row = 0; row < TT; row++) {
         const int j = tile * TT + row;
-        for (int x = 0; x < 2 * BPL; x++) {
-          const int d = 2 * t * BPL + x;
-          if ((st.v[tile_at<HD>(row, d / 16) + d % 16] & 0x7f) != 0x7f) continue;
 #pragma unroll
-          for (int hf = 0; hf < NH; hf++)
-            if (j < see[hf]) {
+        for (int x = 0; x < BPL; x++) {
+          const int d = g * BPL + x;
+          if ((st.v[tile_at<HD>(row, d / 16) + d % 16] & 0x7f) == 0x7f)
 #pragma unroll
-              for (int y = 0; y < 2 * BPL; y++)  // indexes of o are known when compiling
-                if (y == x) o[y % BPL][2 * hf + y / BPL] = __int_as_float(0x7fc00000);
-            }
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int e = 0; e < 2; e++)
+                if (j < see[nt][e]) o[x / 2][nt][2 * (x & 1) + e] = __int_as_float(0x7fc00000);
         }
       }
     }
@@ -416,22 +471,26 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
 
   // ---- join the warps: each row's maxima and sum, then the outputs at the common maximum
 #pragma unroll
-  for (int hf = 0; hf < NH; hf++) {
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-    if (t == 0) st_m[w][g + 8 * hf] = m[hf], st_mv[w][g + 8 * hf] = mv[hf], st_l[w][g + 8 * hf] = l[hf];
-  }
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      float x = l[nt][e];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      const int r = 8 * nt + 2 * t + e;
+      if (g == 0) st_m[w][r] = m[nt][e], st_mv[w][r] = mv[nt][e], st_l[w][r] = x;
+    }
   cp_wait<0>();
   __syncthreads();  // every warp is done with its stages
   float* part = reinterpret_cast<float*>(smem);  // [NW][ROWS][OP]
 #pragma unroll
-  for (int hf = 0; hf < NH; hf++)
+  for (int nt = 0; nt < NT; nt++)
 #pragma unroll
     for (int e = 0; e < 2; e++)
 #pragma unroll
-      for (int j = 0; j < BPL; j += 4)
-        *reinterpret_cast<float4*>(part + ((size_t)w * ROWS + g + 8 * hf) * OP + (2 * t + e) * BPL + j) =
-            make_float4(o[j][2 * hf + e], o[j + 1][2 * hf + e], o[j + 2][2 * hf + e], o[j + 3][2 * hf + e]);
+      for (int i = 0; i < MT; i += 2)
+        *reinterpret_cast<float4*>(part + (w * ROWS + 8 * nt + 2 * t + e) * OP + g * BPL + 2 * i) =
+            make_float4(o[i][nt][e], o[i][nt][2 + e], o[i + 1][nt][e], o[i + 1][nt][2 + e]);
   if (threadIdx.x < ROWS) {
     const int r = threadIdx.x;
     float mm = -INFINITY, mmv = -INFINITY, ll = 0.f;
@@ -443,34 +502,35 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
     cl_m[r] = mm, cl_mv[r] = mmv, cl_l[r] = ll;
   }
   __syncthreads();
-  float* sum = part + (size_t)NW * ROWS * OP;  // [ROWS][HD]
+  float* sum = part + NW * ROWS * OP;  // [ROWS][HD]
   for (int i = threadIdx.x; i < ROWS * HD; i += NW * 32) {
     const int r = i / HD, d = i % HD;
     float x = 0.f;
 #pragma unroll
-    for (int k = 0; k < NW; k++) x = fmaf(st_mv[k][r], part[((size_t)k * ROWS + r) * OP + d], x);
+    for (int k = 0; k < NW; k++) x = fmaf(st_mv[k][r], part[(k * ROWS + r) * OP + d], x);
     sum[i] = x;
   }
   // ---- join the cluster's blocks: block `split` finishes its share of the rows' values
   cg::cluster_group cl = cg::this_cluster();
   if (n_split > 1) cl.sync(); else __syncthreads();
   T* out = reinterpret_cast<T*>(at.o);
-  const int share = (ROWS * HD + n_split - 1) / n_split;
-  for (int i = split * share + threadIdx.x; i < min(ROWS * HD, (split + 1) * share); i += NW * 32) {
+  const int used = min(ROWS, R - row0) * HD, share = (used + n_split - 1) / n_split;
+  for (int i = split * share + threadIdx.x; i < min(used, (split + 1) * share); i += NW * 32) {
     const int r = i / HD, d = i % HD, rr = row0 + r;
-    if (rr >= R) break;
     float mm = -INFINITY, mmv = -INFINITY, ll = 0.f, x = 0.f;
-    for (int k = 0; k < n_split; k++) {
-      mm = fmaxf(mm, *(n_split > 1 ? cl.map_shared_rank(&cl_m[r], k) : &cl_m[r]));
-      mmv = fmaxf(mmv, *(n_split > 1 ? cl.map_shared_rank(&cl_mv[r], k) : &cl_mv[r]));
-    }
-    for (int k = 0; k < n_split; k++) {
-      const float km = *(n_split > 1 ? cl.map_shared_rank(&cl_m[r], k) : &cl_m[r]);
-      const float kv = *(n_split > 1 ? cl.map_shared_rank(&cl_mv[r], k) : &cl_mv[r]);
-      const float kl = *(n_split > 1 ? cl.map_shared_rank(&cl_l[r], k) : &cl_l[r]);
-      const float kx = *(n_split > 1 ? cl.map_shared_rank(&sum[i], k) : &sum[i]);
-      ll += km == -INFINITY ? kl : kl * sfu_exp2(km - mm);
-      x += kv == -INFINITY ? kx : kx * sfu_exp2(kv - mmv);
+    if (n_split == 1) {
+      mm = cl_m[r], mmv = cl_mv[r], ll = cl_l[r], x = sum[i];
+    } else {
+      for (int k = 0; k < n_split; k++) {
+        mm = fmaxf(mm, *cl.map_shared_rank(&cl_m[r], k));
+        mmv = fmaxf(mmv, *cl.map_shared_rank(&cl_mv[r], k));
+      }
+      for (int k = 0; k < n_split; k++) {
+        const float km = *cl.map_shared_rank(&cl_m[r], k), kv = *cl.map_shared_rank(&cl_mv[r], k);
+        const float kl = *cl.map_shared_rank(&cl_l[r], k), kx = *cl.map_shared_rank(&sum[i], k);
+        ll += km == -INFINITY ? kl : kl * sfu_exp2(km - mm);
+        x += kv == -INFINITY ? kx : kx * sfu_exp2(kv - mmv);
+      }
     }
     // a row that sees nothing: zeros, and the log of an empty sum
     const float y = ll == 0.f ? 0.f : x / ll * exp2f(mmv - mm);
@@ -487,10 +547,11 @@ __global__ void __launch_bounds__(NW * 32) k_kv8_attn(Kv8Args a, AttnArgs at) {
 
 // weight[slot] += sum over the rows of exp(score - lse): the QK product again,
 // now with the rows' final statistics, so that a slot's sum is formed by one
-// lane in a fixed order.  HBM-bound on K; a warp holds the codes of TW tiles in
-// registers and takes all rows past them.
-template <typename T, int HD, int TW>
+// warp in a fixed order.  A warp holds the codes of TW tiles in registers and
+// takes all rows past them.
+template <typename T, int HD, int NT, int TW>
 __global__ void __launch_bounds__(256) k_kv8_accumulate(Kv8Args a, AttnArgs at) {
+  constexpr int ROWS = 8 * NT, KS = HD / 16;
   const int h = blockIdx.y, s = blockIdx.z;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   int r0;
@@ -498,113 +559,101 @@ __global__ void __launch_bounds__(256) k_kv8_accumulate(Kv8Args a, AttnArgs at) 
   const int cap = a.max_blocks << a.lgP, see_hi = min(len + n, cap);
   if (n == 0) return;
   // the grid covers the caller's bound on the lengths; a longer sequence takes its blocks further
-  for (long at_slot = (long)(blockIdx.x * (blockDim.x >> 5) + w) * TW * TT; at_slot < see_hi;
-       at_slot += (long)gridDim.x * (blockDim.x >> 5) * TW * TT) {
-    const int base = (int)at_slot;
-    uint32_t kw[TW][4][HD / 16];
-    size_t bh[TW][2];   // (block, head) of each group
-    float ks[TW][2];
-    bool ok[TW][2];
+  for (long first = (long)(blockIdx.x * (blockDim.x >> 5) + w) * TW * TT; first < see_hi;
+       first += (long)gridDim.x * (blockDim.x >> 5) * TW * TT) {
+    const int base = (int)first;
+    uint32_t kw[2 * TW][2][KS];
+    int blk[2 * TW];
+    float ks[2 * TW];
 #pragma unroll
-    for (int x = 0; x < TW; x++)
+    for (int x = 0; x < 2 * TW; x++) blk[x] = base + x * 16 < see_hi ? kv8_block(a, s, (base + x * 16) >> a.lgP) : -1;
 #pragma unroll
-      for (int gr = 0; gr < 2; gr++) {
-        const int j0 = base + x * TT + gr * 16;
-        const int b = j0 < see_hi ? kv8_block(a, s, j0 >> a.lgP) : -1;
-        ok[x][gr] = b >= 0;
-        bh[x][gr] = (size_t)max(b, 0) * a.H + h;
-      }
+    for (int x = 0; x < 2 * TW; x++) {
+      const size_t bh = (size_t)max(blk[x], 0) * a.H + h;
+      ks[x] = blk[x] >= 0 ? a.ks[bh] : 0.f;
 #pragma unroll
-    for (int x = 0; x < TW; x++)
+      for (int half = 0; half < 2; half++) {
+        const int j = base + x * 16 + key_token(g, half);
+        const uint8_t* p = a.k + ((bh << a.lgP) + (j & (a.P - 1))) * HD;
+        const bool on = blk[x] >= 0 && j < see_hi;
+        if (HD == 32) {
+          const uint2 c = on ? *reinterpret_cast<const uint2*>(p + t * 8) : make_uint2(0, 0);
+          kw[x][half][0] = c.x, kw[x][half][1] = c.y;
+        } else {
 #pragma unroll
-      for (int gr = 0; gr < 2; gr++) {
-        const int j0 = base + x * TT + gr * 16;
-        ks[x][gr] = ok[x][gr] ? a.ks[bh[x][gr]] : 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 2; nt++) {
-          const int j = j0 + key_token(g, nt);
-          const uint8_t* p = a.k + (bh[x][gr] * a.P + (j & (a.P - 1))) * HD;
-          const bool on = ok[x][gr] && j < see_hi;
-          if (HD == 32) {
-            const uint2 c = on ? *reinterpret_cast<const uint2*>(p + t * 8) : make_uint2(0, 0);
-            kw[x][2 * gr + nt][0] = c.x, kw[x][2 * gr + nt][1] = c.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < HD / 64; i++) {
-              const uint4 c = on ? *reinterpret_cast<const uint4*>(p + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-              kw[x][2 * gr + nt][(4 * i) % (HD / 16)] = c.x, kw[x][2 * gr + nt][(4 * i + 1) % (HD / 16)] = c.y;
-              kw[x][2 * gr + nt][(4 * i + 2) % (HD / 16)] = c.z, kw[x][2 * gr + nt][(4 * i + 3) % (HD / 16)] = c.w;
-            }
+          for (int i = 0; i < HD / 64; i++) {
+            const uint4 c = on ? *reinterpret_cast<const uint4*>(p + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+            kw[x][half][(4 * i) % KS] = c.x, kw[x][half][(4 * i + 1) % KS] = c.y;
+            kw[x][half][(4 * i + 2) % KS] = c.z, kw[x][half][(4 * i + 3) % KS] = c.w;
           }
         }
       }
-    float sum[TW][4][2];
-#pragma unroll
-    for (int x = 0; x < TW; x++)
-#pragma unroll
-      for (int nt = 0; nt < 4; nt++) sum[x][nt][0] = sum[x][nt][1] = 0.f;
-    for (int row0 = 0; row0 < R; row0 += 16) {
-      if (base >= len + min(R - 1, row0 + 15) / G + 1) continue;  // no row of these sees the warp's slots
-      QFrag<T, HD, false> q;
-      q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld, at.q_ld, h * G * HD, G, row0, R, at.scale);
-      float ls[2];
-      int see[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; hf++) {
-        const int r = row0 + g + 8 * hf, i = min(r, R - 1) / G;
-        see[hf] = r < R ? min(len + i + 1, cap) : 0;  // rows past the last see nothing
-        const float x = r < R ? at.lse[(long)(r0 + i) * (a.H * G) + h * G + r % G] : 0.f;
-        if (x == -INFINITY) see[hf] = 0;  // a row without weights
-        ls[hf] = x * 1.4426950408889634f;
-      }
-#pragma unroll
-      for (int x = 0; x < TW; x++)
-#pragma unroll
-        for (int nt = 0; nt < 4; nt++) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          q.qk(d, kw[x][nt]);
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const int j = base + x * TT + (nt >> 1) * 16 + col_token(t, nt & 1, e);
-            const float k = ks[x][nt >> 1];
-            const float p0 = j < see[0] ? sfu_exp2(d[e] * (q.f0 * k) - ls[0]) : 0.f;
-            const float p1 = j < see[1] ? sfu_exp2(d[2 + e] * (q.f1 * k) - ls[1]) : 0.f;
-            sum[x][nt][e] += p0 + p1;
-          }
-        }
     }
+    float sum[2 * TW][2];
 #pragma unroll
-    for (int x = 0; x < TW; x++)
+    for (int x = 0; x < 2 * TW; x++) sum[x][0] = sum[x][1] = 0.f;
+    for (int row0 = 0; row0 < R; row0 += ROWS) {
+      if (base >= len + min(R - 1, row0 + ROWS - 1) / G + 1) continue;  // no row of these sees the warp's slots
+      QFrag<T, HD, NT> q;
+      q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, row0, R, at.scale);
+      float ls[NT][2];
+      int see[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < 4; nt++)
+      for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          float v = sum[x][nt][e];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          const int j = base + x * TT + (nt >> 1) * 16 + col_token(t, nt & 1, e);
-          // one lane of the eight that hold the sum adds it (atomically: two sequences may share a block)
-          if (g == 2 * nt + e && j < see_hi && ok[x][nt >> 1])
-            atomicAdd(a.w + bh[x][nt >> 1] * a.P + (j & (a.P - 1)), v);
+          const int r = row0 + 8 * nt + 2 * t + e, i = min(r, R - 1) / G;
+          see[nt][e] = r < R ? min(len + i + 1, cap) : 0;  // rows past the last see nothing
+          const float x = r < R ? at.lse[(long)(r0 + i) * (a.H * G) + h * G + r % G] : 0.f;
+          if (x == -INFINITY) see[nt][e] = 0;  // a row without weights
+          ls[nt][e] = x * 1.4426950408889634f;
         }
+#pragma unroll
+      for (int x = 0; x < 2 * TW; x++) {
+        float d[NT][4];
+        q.qk(d, kw[x][0], kw[x][1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const int j = base + x * 16 + key_token(g, half);
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+              sum[x][half] += j < see[nt][e] ? sfu_exp2(d[nt][2 * half + e] * (q.f[nt][e] * ks[x]) - ls[nt][e]) : 0.f;
+          }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2 * TW; x++)
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        float v = sum[x][half];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        const int j = base + x * 16 + key_token(g, half);
+        // one of the four lanes that hold the sum adds it (atomically: two sequences may share a block)
+        if (t == half && j < see_hi && blk[x] >= 0)
+          atomicAdd(a.w + ((((size_t)blk[x] * a.H + h) << a.lgP) + (j & (a.P - 1))), v);
+      }
   }
 }
 
-template <typename T, int HD, bool R8>
-bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, long row_tiles, int max_len) {
-  constexpr int NW = 8, NS = HD == 128 ? 3 : 4, ROWS = R8 ? 8 : 16;
-  constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)NW * ROWS * (HD + 4) * 4 + ROWS * HD * 4;
+template <typename T, int HD, int NT, int NS, int MINB>
+bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, int max_len) {
+  constexpr int NW = 4, ROWS = 8 * NT;
+  constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)(NW * ROWS * (HD + 4) + ROWS * HD) * 4;
   const size_t smem = ring > join ? ring : join;
-  auto k = k_kv8_attn<T, HD, R8, NW, NS>;
+  auto k = k_kv8_attn<T, HD, NT, NW, NS, MINB>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
   // few blocks: the slots of each are split over a cluster of up to 8, each with a tile or more for every warp
+  const long row_tiles = ((long)a.max_new * at.G + ROWS - 1) / ROWS;
   const long blocks = (long)a.S * a.H * row_tiles;
   const long tiles = (max_len + TT - 1) / TT;
-  const long want = (2 * c.num_sms + blocks - 1) / blocks, most = (tiles + NW - 1) / NW;
+  const long want = ((long)MINB * c.num_sms + blocks - 1) / blocks, most = (tiles + NW - 1) / NW;
   int split = (int)(want < most ? want : most);
   split = split < 1 ? 1 : split > 8 ? 8 : split;
-  cudaLaunchConfig_t cfg = {};
   at.n_split = split;
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split * row_tiles), a.H, a.S);
   cfg.blockDim = dim3(NW * 32);
   cfg.dynamicSmemBytes = smem;
@@ -621,15 +670,24 @@ bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, long row_tiles, int max_
 template <typename T, int HD>
 bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long rows = (long)a.max_new * at.G;
-  if (rows <= 8) return launch_attn<T, HD, true>(c, a, at, 1, max_len);
-  return launch_attn<T, HD, false>(c, a, at, (rows + 15) / 16, max_len);
+  constexpr int NS = HD == 128 ? 2 : HD == 64 ? 3 : 4;
+  if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : 4>(c, a, at, max_len);
+  if constexpr (HD < 128) {  // 32 rows of 128 dimensions do not fit in the registers
+    if (rows > 16) return launch_attn<T, HD, 4, NS, 2>(c, a, at, max_len);
+  }
+  return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : 3>(c, a, at, max_len);
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int NT>
 void launch_accumulate(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   constexpr int TW = HD == 128 ? 1 : 2;
   const int per = 8 * TW * TT;
-  k_kv8_accumulate<T, HD, TW><<<dim3((max_len + per - 1) / per, a.H, a.S), 256, 0, c.stream>>>(a, at);
+  k_kv8_accumulate<T, HD, NT, TW><<<dim3((max_len + per - 1) / per, a.H, a.S), 256, 0, c.stream>>>(a, at);
+}
+template <typename T, int HD>
+void launch_accumulate_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  if ((long)a.max_new * at.G <= 8) return launch_accumulate<T, HD, 1>(c, a, at, max_len);
+  return launch_accumulate<T, HD, 2>(c, a, at, max_len);
 }
 
 }  // namespace
@@ -653,13 +711,13 @@ void kv8_accumulate(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, con
   LaunchScope s(c, "kv8_accumulate");
   AttnArgs at{q, q_ld, scale, G, 0, nullptr, 0, const_cast<float*>(lse)};
   if (bf16_rows) {
-    if (hd == 32) return launch_accumulate<bf16, 32>(c, a, at, max_len);
-    if (hd == 64) return launch_accumulate<bf16, 64>(c, a, at, max_len);
-    return launch_accumulate<bf16, 128>(c, a, at, max_len);
+    if (hd == 32) return launch_accumulate_rows<bf16, 32>(c, a, at, max_len);
+    if (hd == 64) return launch_accumulate_rows<bf16, 64>(c, a, at, max_len);
+    return launch_accumulate_rows<bf16, 128>(c, a, at, max_len);
   }
-  if (hd == 32) return launch_accumulate<float, 32>(c, a, at, max_len);
-  if (hd == 64) return launch_accumulate<float, 64>(c, a, at, max_len);
-  return launch_accumulate<float, 128>(c, a, at, max_len);
+  if (hd == 32) return launch_accumulate_rows<float, 32>(c, a, at, max_len);
+  if (hd == 64) return launch_accumulate_rows<float, 64>(c, a, at, max_len);
+  return launch_accumulate_rows<float, 128>(c, a, at, max_len);
 }
 
 }  // namespace gpt
