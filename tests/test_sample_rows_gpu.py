@@ -73,6 +73,21 @@ def test_shapes_of_rows(kind, dtype):
     check(torch.from_numpy(z.astype(np.float32)).to(DT[dtype]).cuda(), params(rng, rows), rng.random(rows).astype(np.float32))
 
 
+@pytest.mark.parametrize("dtype,rows,V,ld,sigma", [
+    ("fp32", 2, 50257, 50257, 0.02), ("fp32", 160, 30011, 30011, 0.02), ("bf16", 3, 90001, 90001, 0.05),
+    ("fp32", 2, 400003, 400003, 2.0), ("fp32", 1, 524288, 524288, 0.01), ("bf16", 2, 524287, 524288, 3.0)])
+def test_crowded_borders_and_long_rows(dtype, rows, V, ld, sigma):
+    """Rows whose border lies among thousands of nearly equal tokens, over one block and over clusters, and rows that
+    do not fit in the blocks' memory; the second row starts at an odd offset."""
+    rng = np.random.default_rng(V + rows)
+    z = torch.from_numpy((rng.standard_normal((rows, ld)) * sigma).astype(np.float32)).to(DT[dtype]).cuda()
+    par = {"temperature": rng.choice([0.7, 1.0], rows).astype(np.float32),
+           "top_k": np.where(np.arange(rows) % 3 == 1, V // 3, 0).astype(np.int32),
+           "top_p": np.where(np.arange(rows) % 3 != 1, rng.choice([0.5, 0.9, 0.9999], rows), 1.0).astype(np.float32),
+           "min_p": np.zeros(rows, np.float32)}
+    check(z, par, rng.random(rows).astype(np.float32), V)
+
+
 def test_infinities_nan_and_empty_rows():
     rng = np.random.default_rng(3)
     V = 700
