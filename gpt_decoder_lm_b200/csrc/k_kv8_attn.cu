@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
 
 // weight[slot] += sum over the rows of exp(score - lse): the QK product again,
 // now with the rows' final statistics, so that a slot's sum is formed by one
-// warp in a fixed order.  A warp holds the codes of TW tiles in registers and
-// takes all rows past them.
+// warp in a fixed order.  Here a warp holds the codes of TW tiles in registers
+// and takes all rows past them; k_kv8_accumulate_few has the rows in registers.
 template <typename T, int HD, int NT, int TW>
 __global__ void __launch_bounds__(256) k_kv8_accumulate(Kv8Args a, AttnArgs at) {
   constexpr int ROWS = 8 * NT, KS = HD / 16;
@@ -638,6 +638,115 @@ __global__ void __launch_bounds__(256) k_kv8_accumulate(Kv8Args a, AttnArgs at) 
   }
 }
 
+// At most 8 NT rows (a decoding step): their operand is made once, and each warp
+// of a (sequence, head) takes every so-manieth tile of 32 tokens, with the next
+// tile's codes on their way and the block ids of the one behind it looked up.
+template <typename T, int HD, int NT, int MINB>
+__global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, AttnArgs at) {
+  constexpr int KS = HD / 16;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warps = gridDim.x * 4, first = blockIdx.x * 4 + (threadIdx.x >> 5);
+  int r0;
+  const int n = kv8_rows(a, s, &r0), len = kv8_len(a, s), G = at.G, R = n * G;
+  const int cap = a.max_blocks << a.lgP, see_hi = min(len + n, cap);
+  if (n == 0) return;
+
+  auto look = [&](int tile, int (&b)[2]) {
+#pragma unroll
+    for (int gr = 0; gr < 2; gr++) {
+      const int j = tile * TT + gr * 16;
+      b[gr] = j < see_hi ? a.table[(size_t)s * a.max_blocks + (j >> a.lgP)] : -1;
+      if (j < see_hi && (unsigned)b[gr] >= (unsigned)a.n_blocks) b[gr] = -2;
+    }
+  };
+  auto fetch = [&](int tile, const int (&b)[2], uint32_t (&kw)[2][2][KS], float (&ks)[2]) {
+#pragma unroll
+    for (int gr = 0; gr < 2; gr++) {
+      const size_t bh = (size_t)max(b[gr], 0) * a.H + h;
+      ks[gr] = b[gr] >= 0 ? a.ks[bh] : 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        const int j = tile * TT + gr * 16 + key_token(g, half);
+        const uint8_t* p = a.k + ((bh << a.lgP) + (j & (a.P - 1))) * HD;
+        const bool on = b[gr] >= 0 && j < see_hi;
+        if (HD == 32) {
+          const uint2 c = on ? *reinterpret_cast<const uint2*>(p + t * 8) : make_uint2(0, 0);
+          kw[gr][half][0] = c.x, kw[gr][half][1] = c.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < HD / 64; i++) {
+            const uint4 c = on ? *reinterpret_cast<const uint4*>(p + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+            kw[gr][half][(4 * i) % KS] = c.x, kw[gr][half][(4 * i + 1) % KS] = c.y;
+            kw[gr][half][(4 * i + 2) % KS] = c.z, kw[gr][half][(4 * i + 3) % KS] = c.w;
+          }
+        }
+      }
+    }
+  };
+  uint32_t kw[2][2][KS];
+  float ks[2];
+  int blk[2], ahead[2];
+  look(first, blk);
+  look(first + warps, ahead);
+  fetch(first, blk, kw, ks);
+  QFrag<T, HD, NT> q;
+  q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, 0, R, at.scale);
+  float ls[NT][2];
+  int see[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const int r = 8 * nt + 2 * t + e, i = min(r, R - 1) / G;
+      see[nt][e] = r < R ? min(len + i + 1, cap) : 0;  // rows past the last see nothing
+      const float x = r < R ? at.lse[(long)(r0 + i) * (a.H * G) + h * G + r % G] : 0.f;
+      if (x == -INFINITY) see[nt][e] = 0;  // a row without weights
+      ls[nt][e] = x * 1.4426950408889634f;
+    }
+
+  for (int tile = first; tile * TT < see_hi; tile += warps) {
+    uint32_t kn[2][2][KS];
+    float kns[2];
+    const int now[2] = {blk[0], blk[1]};
+    fetch(tile + warps, ahead, kn, kns);
+    blk[0] = ahead[0], blk[1] = ahead[1];
+    look(tile + 2 * warps, ahead);
+#pragma unroll
+    for (int gr = 0; gr < 2; gr++) {
+      float d[NT][4], sum[2] = {0.f, 0.f};
+      q.qk(d, kw[gr][0], kw[gr][1]);
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          const int j = tile * TT + gr * 16 + key_token(g, half);
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+            sum[half] += j < see[nt][e] ? sfu_exp2(d[nt][2 * half + e] * (q.f[nt][e] * ks[gr]) - ls[nt][e]) : 0.f;
+        }
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
+        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
+      }
+      if (now[gr] == -2 && lane == 0) kv8_flag(a, FLAG_BLOCK);
+      // one of the four lanes that hold a sum adds it (atomically: two sequences may share a block)
+      const int j = tile * TT + gr * 16 + key_token(g, t & 1);
+      if (t < 2 && j < see_hi && now[gr] >= 0)
+        atomicAdd(a.w + ((((size_t)now[gr] * a.H + h) << a.lgP) + (j & (a.P - 1))), t ? sum[1] : sum[0]);
+    }
+#pragma unroll
+    for (int gr = 0; gr < 2; gr++) {
+      ks[gr] = kns[gr];
+#pragma unroll
+      for (int half = 0; half < 2; half++)
+#pragma unroll
+        for (int i = 0; i < KS; i++) kw[gr][half][i] = kn[gr][half][i];
+    }
+  }
+}
+
 template <typename T, int HD, int NT, int NS, int MINB>
 bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, int max_len) {
   constexpr int NW = 4, ROWS = 8 * NT;
@@ -684,9 +793,20 @@ void launch_accumulate(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len
   const int per = 8 * TW * TT;
   k_kv8_accumulate<T, HD, NT, TW><<<dim3((max_len + per - 1) / per, a.H, a.S), 256, 0, c.stream>>>(a, at);
 }
+template <typename T, int HD, int NT>
+void launch_accumulate_few(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  constexpr int MINB = HD == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 6 : 4;
+  // a warp for every two tiles, or as many blocks as the GPU holds
+  const long tiles = (max_len + TT - 1) / TT, most = (tiles + 7) / 8, pairs = (long)a.H * a.S;
+  long split = ((long)MINB * c.num_sms + pairs - 1) / pairs;
+  split = split > most ? most : split;
+  k_kv8_accumulate_few<T, HD, NT, MINB><<<dim3((unsigned)split, a.H, a.S), 128, 0, c.stream>>>(a, at);
+}
 template <typename T, int HD>
 void launch_accumulate_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
-  if ((long)a.max_new * at.G <= 8) return launch_accumulate<T, HD, 1>(c, a, at, max_len);
+  const long rows = (long)a.max_new * at.G;
+  if (rows <= 8) return launch_accumulate_few<T, HD, 1>(c, a, at, max_len);
+  if (rows <= 16) return launch_accumulate_few<T, HD, 2>(c, a, at, max_len);
   return launch_accumulate<T, HD, 2>(c, a, at, max_len);
 }
 
