@@ -332,26 +332,37 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
     const int ok = st.ok;
     const bool full = tile * TT + TT <= see_lo && ok == 3;
     const float k0 = st.ks[0], k1 = st.ks[1];
-    // log2 of the V scales; a group without tokens has none
-    const float v0 = ok & 1 ? __log2f(st.vs[0]) : -INFINITY, v1 = ok & 2 ? __log2f(st.vs[1]) : -INFINITY;
+    // log2 of the V scales (powers of two); a group without tokens has none
+    const float v0 = ok & 1 ? (float)((int)(__float_as_uint(st.vs[0]) >> 23) - 127) : -INFINITY;
+    const float v1 = ok & 2 ? (float)((int)(__float_as_uint(st.vs[1]) >> 23) - 127) : -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+#pragma unroll
+        for (int gr = 0; gr < 2; gr++) {
+          const float f = q.f[nt][e] * (gr ? k1 : k0);
+          sc[gr][nt][e] *= f;
+          sc[gr][nt][2 + e] *= f;
+        }
+    if (!full) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+          for (int gr = 0; gr < 2; gr++)
+#pragma unroll
+            for (int half = 0; half < 2; half++)
+              if (tile * TT + gr * 16 + key_token(g, half) >= see[nt][e] || !(ok >> gr & 1)) sc[gr][nt][2 * half + e] = -INFINITY;
+    }
     bool grow = false;
     float top[NT][2], topv[NT][2];  // largest score, and score + log2 V scale
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        float big[2];
-#pragma unroll
-        for (int gr = 0; gr < 2; gr++) {
-          const float f = q.f[nt][e] * (gr ? k1 : k0);
-#pragma unroll
-          for (int half = 0; half < 2; half++) {
-            float& x = sc[gr][nt][2 * half + e];
-            x *= f;
-            if (!full && (tile * TT + gr * 16 + key_token(g, half) >= see[nt][e] || !(ok >> gr & 1))) x = -INFINITY;
-          }
-          big[gr] = fmaxf(sc[gr][nt][e], sc[gr][nt][2 + e]);
-        }
+        const float big[2] = {fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])};
         float x = fmaxf(big[0], big[1]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
     for (int e = 0; e < 2; e++)
 #pragma unroll
       for (int i = 0; i < MT; i += 2)
-        *reinterpret_cast<float4*>(part + (w * ROWS + 8 * nt + 2 * t + e) * OP + g * BPL + 2 * i) =
+        if (8 * nt + 2 * t + e < R - row0) *reinterpret_cast<float4*>(part + (w * ROWS + 8 * nt + 2 * t + e) * OP + g * BPL + 2 * i) =
             make_float4(o[i][nt][e], o[i][nt][2 + e], o[i + 1][nt][e], o[i + 1][nt][2 + e]);
   if (threadIdx.x < ROWS) {
     const int r = threadIdx.x;
@@ -503,7 +514,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   }
   __syncthreads();
   float* sum = part + NW * ROWS * OP;  // [ROWS][HD]
-  for (int i = threadIdx.x; i < ROWS * HD; i += NW * 32) {
+  const int used = min(ROWS, R - row0) * HD;
+  for (int i = threadIdx.x; i < used; i += NW * 32) {
     const int r = i / HD, d = i % HD;
     float x = 0.f;
 #pragma unroll
@@ -514,7 +526,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   cg::cluster_group cl = cg::this_cluster();
   if (n_split > 1) cl.sync(); else __syncthreads();
   T* out = reinterpret_cast<T*>(at.o);
-  const int used = min(ROWS, R - row0) * HD, share = (used + n_split - 1) / n_split;
+  const int share = (used + n_split - 1) / n_split;
   for (int i = split * share + threadIdx.x; i < min(used, (split + 1) * share); i += NW * 32) {
     const int r = i / HD, d = i % HD, rr = row0 + r;
     float mm = -INFINITY, mmv = -INFINITY, ll = 0.f, x = 0.f;
@@ -779,12 +791,12 @@ bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, int max_len) {
 template <typename T, int HD>
 bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long rows = (long)a.max_new * at.G;
-  constexpr int NS = HD == 128 ? 2 : HD == 64 ? 3 : 4;
-  if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : 4>(c, a, at, max_len);
-  if constexpr (HD < 128) {  // 32 rows of 128 dimensions do not fit in the registers
-    if (rows > 16) return launch_attn<T, HD, 4, NS, 2>(c, a, at, max_len);
-  }
-  return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : 3>(c, a, at, max_len);
+  // Stages a warp and blocks an SM, by trial: with 64 dimensions and 8 rows two stages and five blocks took 21.3 us for
+  // 64 sequences of 12 heads, three and four 24.5 us; with 16 rows two and four 43 us for a prompt's next part, 32 rows
+  // in three and two 58 us.
+  constexpr int NS = HD == 32 ? 4 : 2;
+  if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
+  return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
 }
 
 template <typename T, int HD, int NT>
