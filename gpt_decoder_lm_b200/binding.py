@@ -90,6 +90,7 @@ _PROTOS = {
     "gpt_eval_loss": (I32, [P, P, U64, U64, I32, P]),
     "gpt_sample": (I32, [P, I32, I32, I32, I64, F32, I32, F32, P, P, P]),
     "gpt_generate": (I32, [P, P, I32, I32, F32, I32, F32, P, P]),
+    "gpt_generate_kv8": (I32, [P, P, P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P]),
     "gpt_sample_rows": (I32, [P, I32, I32, I32, I64, P, P, P, P, P, P, P, P]),
     "gpt_kv8_append": (I32, [P, P, I32, I32, I32, P, I64, P, I64, P]),
     "gpt_kv8_attention": (I32, [P, P, I32, I32, I32, I32, P, I64, F32, I32, P, I64, P, P]),
@@ -381,6 +382,35 @@ class Model:
         out: device int32 [batch_size, T0 + n_new]."""
         _check(lib().gpt_generate(self.h, _ptr(prompt), prompt.shape[1], n_new, temperature, top_k, top_p,
                                   _ptr(uniform), _ptr(out)), self.h, "generate")
+
+    def generate_kv8(self, cache: "KV8Cache", prompt, n_new: int, uniform, out, prompt_len=None, budget: int = 0,
+                     recent: int = 0, table_out=None, kept=None, temperature=None, top_k=None, top_p=None, min_p=None,
+                     logp=None) -> int:
+        """gpt_generate_kv8.  cache: n_layer * batch_size sequences; prompt: device int32 [batch_size, T0]; prompt_len:
+        int32 [batch_size]; uniform: float32 [n_new, batch_size]; out int32 and logp float32 [batch_size, n_new];
+        temperature, top_p, min_p float32, top_k int32: [batch_size]; with budget > 0, table_out int32 like the cache's
+        table and kept int32 [sequences, heads, budget].  Returns how often it evicted; after an odd number the cache's
+        table is table_out."""
+        import torch
+        B = self.cfg.batch_size
+        f32, i32 = torch.float32, torch.int32
+        _require(prompt.dim() == 2 and cache.n_seq == self.cfg.n_layer * B,
+                 "generate_kv8: prompt is [batch_size, T0], the cache has n_layer * batch_size sequences")
+        for t, shape, dtype, name in ((prompt, (B, prompt.shape[1]), i32, "prompt"), (prompt_len, (B,), i32, "prompt_len"),
+                                      (uniform, (n_new, B), f32, "uniform"), (out, (B, n_new), i32, "out"),
+                                      (logp, (B, n_new), f32, "logp"), (temperature, (B,), f32, "temperature"),
+                                      (top_k, (B,), i32, "top_k"), (top_p, (B,), f32, "top_p"), (min_p, (B,), f32, "min_p"),
+                                      (table_out, tuple(cache.table.shape), i32, "table_out"),
+                                      (kept, (cache.n_seq, cache.n_head_kv, budget), i32, "kept")):
+            _require(t is None or (tuple(t.shape) == shape and t.dtype == dtype and t.is_contiguous() and
+                                   t.device == cache.device), f"generate_kv8: {name} has another shape, type, layout or device")
+        n = C.c_int32()
+        _check(lib().gpt_generate_kv8(self.h, cache._ref, _ptr(prompt), _ptr(prompt_len), prompt.shape[1], n_new, budget,
+                                      recent, _ptr(table_out), _ptr(kept), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                      _ptr(min_p), _ptr(uniform), _ptr(out), _ptr(logp), C.byref(n)), self.h, "generate_kv8")
+        if n.value % 2:
+            cache.table = table_out
+        return n.value
 
     # -- LoRA adapters on the fused QKV blocks (targets: 1 q, 2 k, 4 v)
     def lora_attach(self, r: int, alpha: float, targets: int, A):

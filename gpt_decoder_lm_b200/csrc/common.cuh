@@ -111,7 +111,7 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // flags (device word in the workspace)
-enum : uint32_t { FLAG_TOKEN = 1u, FLAG_LOSS = 2u, FLAG_NORM = 4u, FLAG_TIMEOUT = 8u };
+enum : uint32_t { FLAG_TOKEN = 1u, FLAG_LOSS = 2u, FLAG_NORM = 4u, FLAG_TIMEOUT = 8u, FLAG_PROMPT_LEN = 128u };
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -16,6 +16,7 @@
 
 #include "../../include/gpt.h"
 #include "kernels.cuh"
+#include "kv8.cuh"
 
 using namespace gpt;
 
@@ -111,6 +112,8 @@ int choose_splits(long M, long N, long K) { return gemm_tc_plan(M, N, K, true, 1
 
 }  // namespace
 
+constexpr int GEN_KEY = 32;  // words that tell one generating call from another
+
 struct gpt_model {
   gpt_config cfg;
   int V, Vp, L, H, d, T, B, ga, hd;
@@ -165,7 +168,7 @@ struct gpt_model {
   int gen_warm = 0;
   bool capturing = false;  // a graph of the step is being captured
   uint64_t gen_launches = 0;
-  uint64_t gen_key[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  uint64_t gen_key[GEN_KEY] = {};  // the generating call that gen_exec holds
   int part_cap = 0;                 // partial rows per norm instance
   float* norm_parts = nullptr;      // [2L+1][part_cap][3][d]
   float* colsum_parts = nullptr;    // [L][2][colsum_rows][4d]
@@ -527,6 +530,7 @@ gpt_status sync_and_flags(gpt_model* m, const char* where, float* h_scal /* 4 fl
   uint32_t fresh = fl & ~m->reported;
   m->reported |= fl;
   if (fresh & FLAG_TIMEOUT) return fail(m, GPT_ERR_TIMEOUT, "%s: a bounded device wait ran out", where);
+  if (fresh & FLAG_PROMPT_LEN) return fail(m, GPT_ERR_INVALID_ARG, "%s: a prompt's length is outside [1, T0]", where);
   if (fresh & FLAG_TOKEN) return fail(m, GPT_ERR_TOKEN_RANGE, "%s: token id outside [0, vocab_size)", where);
   if (fresh & (FLAG_LOSS | FLAG_NORM)) return fail(m, GPT_ERR_NONFINITE, "%s: non-finite loss or gradient norm", where);
   return GPT_OK;
@@ -1051,15 +1055,48 @@ void bias_corrections(const gpt_model* m, int step, float* bc1, float* bc2) {
 
 }  // namespace
 
+// ---------------------------------------------------------------- decoding over the 8-bit cache
+// What the steps of one gpt_generate_kv8 call share.  The cache's sequences are
+// the layers' (layer l's at l * B ..), so that one call evicts or advances all.
+struct Kv8Gen {
+  Kv8Args cache;
+  const int32_t* len;  // the prompts' lengths
+  int bound;           // at least the tokens that a sequence holds, with the step's
+  bool weights;        // accumulate the attention weights
+  Kv8Args step(int l, int B) const {  // layer l's sequences, one new row each
+    Kv8Args a = cache;
+    a.S = B;
+    a.table += (size_t)l * B * a.max_blocks;
+    a.len += (size_t)l * B;
+    a.n_rows = B;
+    a.max_new = 1;
+    return a;
+  }
+};
+
+// Appends the rows' keys and values to a layer's sequences, attends (o not null) and accumulates the weights.
+template <typename T>
+bool kv8_layer(gpt_model* m, const Kv8Args& a, const T* qkv, T* o, int max_len, bool weights) {
+  Ctx& c = m->ctx;
+  const int d = m->d;
+  const bool b16 = sizeof(T) == 2;
+  const float scale = 1.0f / sqrtf((float)m->hd);
+  kv8_append(c, a, m->hd, b16, qkv + d, 3 * d, qkv + 2 * d, 3 * d);
+  if (o && !kv8_attention(c, a, m->hd, 1, b16, qkv, 3 * d, scale, max_len, o, d, weights ? m->lse : nullptr)) return false;
+  if (weights) kv8_accumulate(c, a, m->hd, 1, b16, qkv, 3 * d, scale, max_len, m->lse);
+  return true;
+}
+
 // ============================================================================
 // C ABI
 // ============================================================================
 // One decoding step for every batch row: the token dec_tok[b] at position t
 // goes through the model with the per-layer qkv activations as the key /
 // value cache (this step's K and V are written at position t), leaving the
-// logits of the next token in dec_logits [B, Vp].
+// logits of the next token in dec_logits [B, Vp].  With kv: of sequences of
+// different lengths over an 8-bit cache, t positions behind each prompt's end.
 template <typename T>
-gpt_status decode_step_t(gpt_model* m, int t) {
+gpt_status decode_step_t(gpt_model* m, int t, const Kv8Gen* kv = nullptr) {
   Ctx& c = m->ctx;
   const int B = m->B, d = m->d, L = m->L, Tn = m->T;
   const bool rms = m->micro;
@@ -1089,7 +1126,10 @@ gpt_status decode_step_t(gpt_model* m, int t) {
     norm_fwd<T>(c, m->dec_res, nw, nb, a, m->dec_mean, m->dec_rstd, B, d, rms, eps);
     return gemm(m, g);
   };
-  embed_fwd<T>(c, m->dec_tok, m->P(m->wte), m->P(m->wpe) + (size_t)t * d, m->dec_res, B, 1, d, DropKey{});
+  if (kv)
+    embed_rows(c, m->dec_tok, kv->len, t, Tn, m->V, m->P(m->wte), m->P(m->wpe), m->dec_res, B, d);
+  else
+    embed_fwd<T>(c, m->dec_tok, m->P(m->wte), m->P(m->wpe) + (size_t)t * d, m->dec_res, B, 1, d, DropKey{});
   for (int l = 0; l < L; l++) {
     const LayerP& y = m->layers[l];
     T* qkv = at<T>(m->qkv, l * 3 * Md);
@@ -1097,10 +1137,14 @@ gpt_status decode_step_t(gpt_model* m, int t) {
     g.epi.kind = EPI_BIAS;
     g.name = "gemm_qkv_decode";
     g.epi.bias = y.qkv_b >= 0 ? m->P(y.qkv_b) : nullptr;
-    g.epi.out = qkv + (size_t)t * 3 * d;  // row b at position t of the cache
-    g.epi.ldo = Tn * 3 * d;
+    g.epi.out = kv ? qkv : qkv + (size_t)t * 3 * d;  // row b at position t of the cache; kv: rows beside each other
+    g.epi.ldo = kv ? 3 * d : Tn * 3 * d;
     if (!norm_gemm(y.ln1_w, y.ln1_b, g)) return fail(m, GPT_ERR_CUDA, "decode qkv gemm failed");
-    attn_decode<T>(c, qkv, B, Tn, m->H, m->hd, t, o);
+    if (!kv) {
+      attn_decode<T>(c, qkv, B, Tn, m->H, m->hd, t, o);
+    } else if (!kv8_layer<T>(m, kv->step(l, B), qkv, o, kv->bound, kv->weights)) {
+      return fail(m, GPT_ERR_CUDA, "decode attention failed");
+    }
     g = gd(B, d, d, o, d, true, m->Wop(y.ap_w), d, true);
     g.epi.kind = EPI_RESADD;
     g.name = "gemm_attnproj_decode";
@@ -1136,6 +1180,133 @@ gpt_status decode_step_t(gpt_model* m, int t) {
   g.epi.ldo = m->Vp;
   if (!norm_gemm(m->lnf_w, m->lnf_b, g)) return fail(m, GPT_ERR_CUDA, "decode lm_head gemm failed");
   return check_cuda(m, "decode step");
+}
+
+// The kernels and copies of one gpt_generate_kv8 call, enqueued on the model's stream.
+template <typename T>
+static gpt_status generate_kv8_body(gpt_model* m, const Kv8Args& cache, const int32_t* d_prompt,
+                                    const int32_t* d_prompt_len, int32_t T0, int32_t n_new, int32_t budget,
+                                    int32_t recent, const int32_t* d_table_out, int32_t* d_kept,
+                                    const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                                    const float* d_min_p, const float* d_uniform, int32_t* d_out, float* d_logp) {
+  Ctx& c = m->ctx;
+  const int B = m->B, Tn = m->T, d = m->d;
+  const size_t Md = (size_t)m->M * d;
+  const float saved_drop = m->cfg.dropout;
+  m->cfg.dropout = 0.f;  // inference runs without dropout
+  cudaMemsetAsync(m->stage_tgt, 0, (size_t)m->M * 4, c.stream);
+  // prefill: the padded prompts through the full forward, their lengths in the embedding sort's scratch
+  prompt_rows(c, d_prompt, d_prompt_len, B, T0, Tn, m->stage_idx, m->spos);
+  check_tokens(c, m->stage_idx, m->stage_tgt, m->M, m->V, m->idx, m->tgt);
+  gpt_status s = forward_any(m, false, m->scal + 6, 1.0f / (float)m->M, 0);
+  m->cfg.dropout = saved_drop;
+  if (s != GPT_OK) return s;
+  Kv8Gen kv;
+  kv.cache = cache;
+  kv.len = m->spos;
+  kv.weights = budget > 0;
+  kv.bound = T0;
+  const int capacity = cache.max_blocks << cache.lgP;
+  const int32_t* other = d_table_out;
+  cudaMemsetAsync(cache.len, 0, (size_t)cache.S * 4, c.stream);
+  auto padded = [&](Kv8Args a) {  // the prompts' rows of the forward's activations
+    a.every = Tn;
+    a.count = kv.len;
+    a.n_count = B;
+    a.n_rows = m->M;
+    a.max_new = T0;
+    return a;
+  };
+  for (int l = 0; l < m->L; l++)
+    if (!kv8_layer<T>(m, padded(kv.step(l, B)), at<T>(m->qkv, l * 3 * Md), kv.weights ? at<T>(m->atto, l * Md) : nullptr, T0,
+                      kv.weights))
+      return fail(m, GPT_ERR_CUDA, "generate_kv8: filling the cache failed");
+  kv8_advance(c, padded(kv.cache), capacity);
+  last_rows(c, m->logits, kv.len, B, Tn, (long)m->Vp * (long)m->asz, m->dec_logits);
+  for (int i = 0;; i++) {
+    if (!sample_rows_each(c, m->dec_logits, m->bf16m, B, m->V, m->Vp, d_temperature, d_top_k, d_top_p, d_min_p,
+                          d_uniform + (size_t)i * B, m->dec_tok, d_logp ? m->row_loss : nullptr))
+      return fail(m, GPT_ERR_CUDA, "generate_kv8: the draw failed");
+    cudaMemcpy2DAsync(d_out + i, (size_t)n_new * 4, m->dec_tok, 4, 4, B, cudaMemcpyDeviceToDevice, c.stream);
+    if (d_logp) cudaMemcpy2DAsync(d_logp + i, (size_t)n_new * 4, m->row_loss, 4, 4, B, cudaMemcpyDeviceToDevice, c.stream);
+    if (i + 1 == n_new) break;
+    if (budget > 0 && kv.bound == capacity) {  // no room for the next token
+      if (!kv8_evict(c, kv.cache, m->hd, other, cache.max_blocks, budget, recent, d_kept))
+        return fail(m, GPT_ERR_CUDA, "generate_kv8: eviction failed");
+      const int32_t* t = kv.cache.table;
+      kv.cache.table = other;
+      other = t;
+      Kv8Args a = kv.cache;  // no new tokens
+      a.n_rows = 0;
+      kv8_advance(c, a, budget);
+      kv.bound = budget;
+    }
+    kv.bound++;
+    s = decode_step_t<T>(m, i, &kv);
+    if (s != GPT_OK) return s;
+    Kv8Args a = kv.cache;
+    a.n_rows = a.S;
+    a.max_new = 1;
+    kv8_advance(c, a, capacity);
+  }
+  return check_cuda(m, "generate_kv8");
+}
+
+// One generating call: a repeated call (the same key: buffers, lengths and
+// parameters) replays a CUDA graph of the whole call; the first such call runs
+// eagerly, the second is captured, later ones replay.
+template <typename F>
+static gpt_status run_generation(gpt_model* m, const uint64_t (&key)[GEN_KEY], const char* what, F body) {
+  Ctx& c = m->ctx;
+  bool replay = m->graphs_on && !c.timing;
+  if (memcmp(key, m->gen_key, sizeof key) != 0) {  // a new call shape starts over
+    if (m->gen_exec) cudaGraphExecDestroy(m->gen_exec);
+    m->gen_exec = nullptr;
+    m->gen_warm = 0;
+    memcpy(m->gen_key, key, sizeof key);
+  }
+  gpt_status s = GPT_OK;
+  if (replay && !m->gen_exec) {
+    if (m->gen_warm < 1) {
+      m->gen_warm++;
+      replay = false;
+    } else {
+      bool ok = m->cap_stream || cudaStreamCreateWithFlags(&m->cap_stream, cudaStreamNonBlocking) == cudaSuccess;
+      cudaStream_t user = c.stream;
+      const uint64_t l0 = c.launches;
+      cudaGraph_t g = nullptr;
+      if (ok) ok = cudaStreamBeginCapture(m->cap_stream, cudaStreamCaptureModeThreadLocal) == cudaSuccess;
+      if (ok) {
+        c.stream = m->cap_stream;
+        s = body();
+        c.stream = user;
+        m->gen_launches = c.launches - l0;
+        ok = cudaStreamEndCapture(m->cap_stream, &g) == cudaSuccess && s == GPT_OK;
+      }
+      if (ok) ok = cudaGraphInstantiate(&m->gen_exec, g, 0) == cudaSuccess;
+      if (g) cudaGraphDestroy(g);
+      c.launches = l0;
+      if (!ok) {
+        cudaGetLastError();
+        m->gen_exec = nullptr;
+        m->gen_warm = 0;
+        m->have_forward = false;
+        if (s != GPT_OK) return s;
+        return fail(m, GPT_ERR_CUDA,
+                    "%s: capturing the call into a CUDA graph failed (nothing ran; "
+                    "gpt_set_graphs(m, 0) runs calls eagerly)", what);
+      }
+    }
+  }
+  if (replay && m->gen_exec) {
+    if (cudaGraphLaunch(m->gen_exec, c.stream) != cudaSuccess) return check_cuda(m, "generate graph launch");
+    c.launches += m->gen_launches;
+  } else {
+    s = body();
+  }
+  m->have_forward = false;
+  if (s != GPT_OK) return s;
+  return sync_and_flags(m, what, nullptr);
 }
 
 extern "C" {
@@ -1678,63 +1849,55 @@ gpt_status gpt_generate(gpt_model* m, const int32_t* d_prompt, int32_t T0, int32
   if (T0 < 1 || n_new < 1 || (long)T0 + n_new > m->T)
     return fail(m, GPT_ERR_INVALID_ARG, "generate: need 1 <= prompt length and prompt + new tokens <= block_size");
   if (m->rc) return fail(m, GPT_ERR_UNSUPPORTED, "generate: the key / value cache needs recompute = 0");
-  Ctx& c = m->ctx;
-  // A repeated call shape (same buffers, lengths and sampling parameters)
-  // replays a CUDA graph of the whole call: the first call runs eagerly, the
-  // second is captured, later ones replay.
-  uint64_t key[8] = {(uint64_t)(uintptr_t)d_prompt, (uint64_t)(uintptr_t)d_uniform, (uint64_t)(uintptr_t)d_out,
-                     (uint64_t)T0, (uint64_t)n_new, 0, (uint64_t)(uint32_t)top_k, 0};
-  memcpy(&key[5], &temperature, 4);
-  memcpy(&key[7], &top_p, 4);
-  bool replay = m->graphs_on && !c.timing;
-  if (memcmp(key, m->gen_key, sizeof key) != 0) {  // a new call shape starts over
-    if (m->gen_exec) cudaGraphExecDestroy(m->gen_exec);
-    m->gen_exec = nullptr;
-    m->gen_warm = 0;
-    memcpy(m->gen_key, key, sizeof key);
+  uint64_t key[GEN_KEY] = {1, (uint64_t)(uintptr_t)d_prompt, (uint64_t)(uintptr_t)d_uniform, (uint64_t)(uintptr_t)d_out,
+                           (uint64_t)T0, (uint64_t)n_new, 0, (uint64_t)(uint32_t)top_k, 0};
+  memcpy(&key[6], &temperature, 4);
+  memcpy(&key[8], &top_p, 4);
+  return run_generation(m, key, "generate", [&] {
+    return generate_body(m, d_prompt, T0, n_new, temperature, top_k, top_p, d_uniform, d_out);
+  });
+}
+
+gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int32_t* d_prompt,
+                            const int32_t* d_prompt_len, int32_t T0, int32_t n_new, int32_t budget, int32_t recent,
+                            const int32_t* d_table_out, int32_t* d_kept, const float* d_temperature,
+                            const int32_t* d_top_k, const float* d_top_p, const float* d_min_p,
+                            const float* d_uniform, int32_t* d_out, float* d_logp, int32_t* h_evictions) {
+  if (!m || !cache || !d_prompt || !d_uniform || !d_out) return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: null argument");
+  if (T0 < 1 || n_new < 1 || (long)T0 + n_new > m->T)
+    return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: need 1 <= prompt length and prompt + new tokens <= block_size");
+  if (m->rc) return fail(m, GPT_ERR_UNSUPPORTED, "generate_kv8: the prompts' keys and values need recompute = 0");
+  Kv8Args a;
+  gpt_status s = kv8_cache_args(cache, &a);
+  if (s != GPT_OK) return fail(m, s, "generate_kv8: the cache's sizes or pointers");
+  if (a.H != m->H || cache->head_dim != m->hd || a.S != m->L * m->B)
+    return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: the cache needs the model's heads and n_layer * batch_size sequences");
+  if (m->V > SAMPLE_MAX_V) return fail(m, GPT_ERR_UNSUPPORTED, "generate_kv8: vocabulary above 524288");
+  const int capacity = a.max_blocks << a.lgP;
+  if (budget < 0 || T0 > capacity || (budget == 0 && T0 + n_new - 1 > capacity))
+    return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: the cache's blocks do not hold the tokens");
+  if (budget > 0 && (budget >= capacity || recent < 0 || recent > budget || !a.w || !d_table_out ||
+                     d_table_out == cache->d_table || !d_kept))
+    return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: eviction needs recent <= budget < capacity, weights and a second table");
+  if (h_evictions) {
+    int n = 0;
+    for (int i = 1, bound = T0; budget > 0 && i < n_new; i++, bound++)
+      if (bound == capacity) n++, bound = budget;
+    *h_evictions = n;
   }
-  gpt_status s = GPT_OK;
-  if (replay && !m->gen_exec) {
-    if (m->gen_warm < 1) {
-      m->gen_warm++;
-      replay = false;
-    } else {
-      bool ok = m->cap_stream || cudaStreamCreateWithFlags(&m->cap_stream, cudaStreamNonBlocking) == cudaSuccess;
-      cudaStream_t user = c.stream;
-      const uint64_t l0 = c.launches;
-      cudaGraph_t g = nullptr;
-      if (ok) ok = cudaStreamBeginCapture(m->cap_stream, cudaStreamCaptureModeThreadLocal) == cudaSuccess;
-      if (ok) {
-        c.stream = m->cap_stream;
-        s = generate_body(m, d_prompt, T0, n_new, temperature, top_k, top_p, d_uniform, d_out);
-        c.stream = user;
-        m->gen_launches = c.launches - l0;
-        ok = cudaStreamEndCapture(m->cap_stream, &g) == cudaSuccess && s == GPT_OK;
-      }
-      if (ok) ok = cudaGraphInstantiate(&m->gen_exec, g, 0) == cudaSuccess;
-      if (g) cudaGraphDestroy(g);
-      c.launches = l0;
-      if (!ok) {
-        cudaGetLastError();
-        m->gen_exec = nullptr;
-        m->gen_warm = 0;
-        m->have_forward = false;
-        if (s != GPT_OK) return s;
-        return fail(m, GPT_ERR_CUDA,
-                    "generate: capturing the call into a CUDA graph failed (nothing ran; "
-                    "gpt_set_graphs(m, 0) runs calls eagerly)");
-      }
-    }
-  }
-  if (replay && m->gen_exec) {
-    if (cudaGraphLaunch(m->gen_exec, c.stream) != cudaSuccess) return check_cuda(m, "generate graph launch");
-    c.launches += m->gen_launches;
-  } else {
-    s = generate_body(m, d_prompt, T0, n_new, temperature, top_k, top_p, d_uniform, d_out);
-  }
-  m->have_forward = false;
-  if (s != GPT_OK) return s;
-  return sync_and_flags(m, "generate", nullptr);
+  uint64_t key[GEN_KEY] = {2, (uint64_t)(uintptr_t)d_prompt, (uint64_t)(uintptr_t)d_prompt_len, (uint64_t)T0,
+                           (uint64_t)n_new, (uint64_t)budget, (uint64_t)recent, (uint64_t)(uintptr_t)d_table_out,
+                           (uint64_t)(uintptr_t)d_kept, (uint64_t)(uintptr_t)d_temperature, (uint64_t)(uintptr_t)d_top_k,
+                           (uint64_t)(uintptr_t)d_top_p, (uint64_t)(uintptr_t)d_min_p, (uint64_t)(uintptr_t)d_uniform,
+                           (uint64_t)(uintptr_t)d_out, (uint64_t)(uintptr_t)d_logp};
+  static_assert(16 * 8 + sizeof(gpt_kv8_cache) <= sizeof key, "the key holds the cache");
+  memcpy(&key[16], cache, sizeof *cache);
+  return run_generation(m, key, "generate_kv8", [&] {
+    return m->bf16m ? generate_kv8_body<bf16>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
+                                              d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp)
+                    : generate_kv8_body<float>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
+                                               d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp);
+  });
 }
 
 gpt_status gpt_eval_loss(gpt_model* m, const void* d_stream, uint64_t stream_len, uint64_t data_seed,

@@ -171,6 +171,67 @@ __global__ void __launch_bounds__(DT) k_attn_decode_v(const T* __restrict__ qkv,
 
 }  // namespace
 
+// ---------------------------------------------------------------- ragged generation
+
+namespace {
+
+// Prompts [B, T0] of len[b] tokens each to the forward's ids [B, T], zeros behind them; the lengths, checked.
+__global__ void k_prompt_rows(const int32_t* __restrict__ prompt, const int32_t* __restrict__ len, int T0, int T,
+                              int32_t* __restrict__ ids, int32_t* __restrict__ len_out, uint32_t* flags) {
+  const int b = blockIdx.x;
+  int n = len ? len[b] : T0;
+  if (n < 1 || n > T0) {
+    if (threadIdx.x == 0) atomicOr(flags, FLAG_PROMPT_LEN);
+    n = min(max(n, 1), T0);
+  }
+  for (int i = threadIdx.x; i < T; i += blockDim.x) ids[(size_t)b * T + i] = i < n ? prompt[(size_t)b * T0 + i] : 0;
+  if (threadIdx.x == 0) len_out[b] = n;
+}
+
+// Row len[b] - 1 of each sequence's T rows.
+template <typename V>
+__global__ void k_last_rows(const V* __restrict__ x, const int32_t* __restrict__ len, int T, long row, V* __restrict__ out) {
+  const int b = blockIdx.y;
+  const V* src = x + ((long)b * T + len[b] - 1) * row;
+  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < row; i += (long)gridDim.x * blockDim.x)
+    out[(long)b * row + i] = src[i];
+}
+
+// wte[tok[b]] + wpe[len[b] + add]
+__global__ void k_embed_rows(const int32_t* __restrict__ tok, const int32_t* __restrict__ len, int add, int T, int V,
+                             const float* __restrict__ wte, const float* __restrict__ wpe, float* __restrict__ res, int d,
+                             uint32_t* flags) {
+  const int b = blockIdx.x;
+  int id = tok[b];
+  if ((unsigned)id >= (unsigned)V) {  // a row of logits that had nothing to draw from
+    if (threadIdx.x == 0) atomicOr(flags, FLAG_TOKEN);
+    id = 0;
+  }
+  const int pos = min(len[b] + add, T - 1);
+  for (int i = threadIdx.x; i < d; i += blockDim.x) res[(size_t)b * d + i] = wte[(size_t)id * d + i] + wpe[(size_t)pos * d + i];
+}
+
+}  // namespace
+
+void prompt_rows(Ctx& c, const int32_t* prompt, const int32_t* len, int B, int T0, int T, int32_t* ids, int32_t* len_out) {
+  LaunchScope s(c, "prompt_rows");
+  k_prompt_rows<<<B, 256, 0, c.stream>>>(prompt, len, T0, T, ids, len_out, c.flags);
+}
+void last_rows(Ctx& c, const void* x, const int32_t* len, int B, int T, long row_bytes, void* out) {
+  LaunchScope s(c, "last_rows");
+  if (row_bytes % 16 == 0)
+    k_last_rows<<<dim3((unsigned)((row_bytes / 16 + 1023) / 1024), B), 256, 0, c.stream>>>(
+        (const uint4*)x, len, T, row_bytes / 16, (uint4*)out);
+  else
+    k_last_rows<<<dim3((unsigned)((row_bytes / 2 + 1023) / 1024), B), 256, 0, c.stream>>>(
+        (const uint16_t*)x, len, T, row_bytes / 2, (uint16_t*)out);
+}
+void embed_rows(Ctx& c, const int32_t* tok, const int32_t* len, int add, int T, int V, const float* wte, const float* wpe,
+                float* res, int B, int d) {
+  LaunchScope s(c, "embed_rows");
+  k_embed_rows<<<B, 256, 0, c.stream>>>(tok, len, add, T, V, wte, wpe, res, d, c.flags);
+}
+
 template <typename T>
 void attn_decode(Ctx& c, const T* qkv, int B, int Tn, int H, int hd, int t, T* o) {
   LaunchScope s(c, "attn_decode");

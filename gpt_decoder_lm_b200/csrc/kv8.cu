@@ -1,16 +1,8 @@
 // C entry points of the 8-bit key / value cache (include/gpt.h, gpt_kv8_*):
 // argument checks, then the launches of k_kv8.cu and k_kv8_attn.cu.
-#include "../../include/gpt.h"
 #include "kv8.cuh"
 
-namespace {
-
-using namespace gpt;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Checks a cache and fills the kernels' arguments.
-gpt_status cache_args(const gpt_kv8_cache* c, Kv8Args* a) {
+gpt_status gpt::kv8_cache_args(const gpt_kv8_cache* c, gpt::Kv8Args* a) {
   if (!c || !c->d_k || !c->d_v || !c->d_k_scale || !c->d_v_scale || !c->d_table || !c->d_len) return GPT_ERR_INVALID_ARG;
   if (c->n_seq < 1 || c->n_head_kv < 1 || c->n_blocks < 1 || c->max_blocks < 1) return GPT_ERR_INVALID_ARG;
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return GPT_ERR_UNSUPPORTED;
@@ -19,8 +11,9 @@ gpt_status cache_args(const gpt_kv8_cache* c, Kv8Args* a) {
   // grid limits, and slots counted in 32 bits
   if (c->n_seq > 65535 || c->n_head_kv > 32767 || (int64_t)c->max_blocks * c->block_tokens > (1 << 30))
     return GPT_ERR_UNSUPPORTED;
+  auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   if (!aligned16(c->d_k) || !aligned16(c->d_v)) return GPT_ERR_INVALID_ARG;
-  *a = Kv8Args{};
+  *a = gpt::Kv8Args{};
   a->S = c->n_seq;
   a->H = c->n_head_kv;
   a->P = c->block_tokens;
@@ -37,6 +30,10 @@ gpt_status cache_args(const gpt_kv8_cache* c, Kv8Args* a) {
   a->flags = c->d_flags;
   return GPT_OK;
 }
+
+namespace {
+
+using namespace gpt;
 
 // The step's rows.
 gpt_status row_args(const int32_t* d_start, int32_t n_rows, int32_t max_new, Kv8Args* a) {
@@ -80,7 +77,7 @@ extern "C" gpt_status gpt_kv8_append(const gpt_kv8_cache* cache, const int32_t* 
                                      int32_t rows_bf16, const void* d_k, int64_t k_ld, const void* d_v, int64_t v_ld,
                                      void* cuda_stream) {
   Kv8Args a;
-  gpt_status st = cache_args(cache, &a);
+  gpt_status st = kv8_cache_args(cache, &a);
   if (st == GPT_OK) st = row_args(d_start, n_rows, max_new, &a);
   if (st != GPT_OK) return st;
   if (!rows_ok(d_k, k_ld, a.H, cache->head_dim, rows_bf16) || !rows_ok(d_v, v_ld, a.H, cache->head_dim, rows_bf16))
@@ -96,7 +93,7 @@ extern "C" gpt_status gpt_kv8_attention(const gpt_kv8_cache* cache, const int32_
                                         int64_t q_ld, float scale, int32_t max_len, void* d_out, int64_t out_ld,
                                         float* d_lse, void* cuda_stream) {
   Kv8Args a;
-  gpt_status st = cache_args(cache, &a);
+  gpt_status st = kv8_cache_args(cache, &a);
   if (st == GPT_OK) st = row_args(d_start, n_rows, max_new, &a);
   if (st != GPT_OK) return st;
   if (n_head < 1 || n_head % a.H || max_len < 0 || !(scale == scale) || !rows_ok(d_q, q_ld, n_head, cache->head_dim, rows_bf16) ||
@@ -115,7 +112,7 @@ extern "C" gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32
                                          int64_t q_ld, float scale, int32_t max_len, const float* d_lse,
                                          void* cuda_stream) {
   Kv8Args a;
-  gpt_status st = cache_args(cache, &a);
+  gpt_status st = kv8_cache_args(cache, &a);
   if (st == GPT_OK) st = row_args(d_start, n_rows, max_new, &a);
   if (st != GPT_OK) return st;
   if (!a.w || !d_lse || n_head < 1 || n_head % a.H || max_len < 0 || !(scale == scale) ||
@@ -133,7 +130,7 @@ extern "C" gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32
 extern "C" gpt_status gpt_kv8_evict(const gpt_kv8_cache* cache, const int32_t* d_table_out, int32_t max_blocks_out,
                                     int32_t budget, int32_t recent, int32_t* d_kept, void* cuda_stream) {
   Kv8Args a;
-  gpt_status st = cache_args(cache, &a);
+  gpt_status st = kv8_cache_args(cache, &a);
   if (st != GPT_OK) return st;
   if (!a.w || !d_table_out || d_table_out == cache->d_table || !d_kept || budget < 1 || recent < 0 || recent > budget ||
       max_blocks_out < 1 || (int64_t)max_blocks_out * a.P < budget)
@@ -146,7 +143,7 @@ extern "C" gpt_status gpt_kv8_evict(const gpt_kv8_cache* cache, const int32_t* d
 extern "C" gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows,
                                       int32_t max_new, int32_t max_len, void* cuda_stream) {
   Kv8Args a;
-  gpt_status st = cache_args(cache, &a);
+  gpt_status st = kv8_cache_args(cache, &a);
   if (st == GPT_OK && max_new > 0) st = row_args(d_start, n_rows, max_new, &a);  // max_new 0: no new tokens
   if (st != GPT_OK) return st;
   const int cap = capacity(a);

@@ -1,6 +1,7 @@
 // The 8-bit key / value cache: what its kernels and its C entry points share.
 #pragma once
 
+#include "../../include/gpt.h"
 #include "kernels.cuh"
 
 namespace gpt {
@@ -26,6 +27,10 @@ struct Kv8Args {
   // the step's new tokens: rows start[s] .. start[s + 1] - 1 (start null: row s)
   const int32_t* start;
   int n_rows, max_new;
+  // ... or, of a padded batch (every > 0): sequence s has the first count[s % n_count] of rows (s % n_count) every ..
+  int every;
+  const int32_t* count;
+  int n_count;
 };
 
 #ifdef __CUDACC__
@@ -36,6 +41,11 @@ __device__ __forceinline__ void kv8_flag(const Kv8Args& a, uint32_t bit) {
 // First row and number of new tokens of sequence s; offsets that descend, leave
 // [0, n_rows] or give a sequence more than max_new count as no tokens.
 __device__ __forceinline__ int kv8_rows(const Kv8Args& a, int s, int* r0) {
+  if (a.every) {
+    const int i = s % a.n_count;
+    *r0 = i * a.every;
+    return min(max(a.count[i], 0), a.max_new);
+  }
   if (!a.start) {
     *r0 = s;
     return s < a.n_rows ? 1 : 0;
@@ -89,6 +99,9 @@ __device__ __forceinline__ uint32_t f16x2_e4m3(uint32_t x) {
   return r;
 }
 #endif
+
+// Checks a cache (host) and fills the kernels' arguments but for the rows.
+gpt_status kv8_cache_args(const gpt_kv8_cache* c, Kv8Args* a);
 
 // dtype of q, k, v rows and outputs: bf16 or fp32
 void kv8_append(Ctx& c, const Kv8Args& a, int hd, bool bf16_rows, const void* k, long k_ld, const void* v, long v_ld);

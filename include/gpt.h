@@ -83,7 +83,8 @@ enum {
   /* gpt_kv8_* (the cache's own flag word, gpt_kv8_cache.d_flags) */
   GPT_FLAG_BLOCK_RANGE = 1u << 4, /* a table entry was outside [0, n_blocks): its tokens were left out */
   GPT_FLAG_CACHE_FULL = 1u << 5,  /* tokens past the table's capacity were not stored                  */
-  GPT_FLAG_ROW_RANGE = 1u << 6    /* offsets were out of order or out of range: a sequence was left out */
+  GPT_FLAG_ROW_RANGE = 1u << 6,   /* offsets were out of order or out of range: a sequence was left out */
+  GPT_FLAG_PROMPT_LENGTH = 1u << 7 /* gpt_generate_kv8: a prompt's length was outside [1, T0]           */
 };
 
 /* Plain-old-data model + optimiser configuration.  Field names follow the
@@ -504,6 +505,39 @@ gpt_status gpt_kv8_evict(const gpt_kv8_cache* cache, const int32_t* d_table_out,
  * max_new 0: n = 0, d_start and n_rows are not used. */
 gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
                            int32_t max_len, void* cuda_stream);
+
+/* gpt_generate over an 8-bit cache, for prompts of different lengths and with
+ * sampling parameters for each row.  cache: n_layer * batch_size sequences
+ * (those of layer l from l * batch_size on), n_head_kv and head_dim the
+ * model's; what it held is dropped (the lengths start at 0), its memory is the
+ * caller's.  d_prompt int32 [batch_size, T0], of row b the first
+ * d_prompt_len[b] (device int32, in [1, T0]; NULL: T0 each); what lies behind
+ * them is not read as tokens.  T0 + n_new <= block_size.  The prompts run
+ * through the forward once; their keys and values are appended to the cache,
+ * and every further token costs one decoding step over it.  Positions go on
+ * counting from each prompt's end.
+ * budget > 0: when the next token would not fit in the table's capacity
+ * (max_blocks * block_tokens), every sequence is brought down to `budget`
+ * slots (gpt_kv8_evict with `recent`, the weights being accumulated from the
+ * prompt on), into the blocks of d_table_out (int32 [n_seq, max_blocks]; blocks
+ * of the same pool that d_table does not name), then back, in turn.
+ * *h_evictions (host, nullable) receives how often that happens: after an odd
+ * number the sequences are in d_table_out's blocks.  d_kept int32 [n_seq,
+ * n_head_kv, budget] holds the last one's slots.  Needs budget < capacity,
+ * recent <= budget, T0 <= capacity.  budget 0: the capacity has to hold T0 +
+ * n_new - 1 tokens; d_table_out and d_kept are not used.
+ * Draws as gpt_sample_rows with d_temperature .. d_min_p [batch_size] (each
+ * nullable) and d_uniform fp32 [n_new, batch_size].  d_out int32 [batch_size,
+ * n_new] receives the new tokens, d_logp (nullable, fp32, the same shape) their
+ * log-probabilities.  The last token drawn is not appended.  Otherwise as
+ * gpt_generate: overwrites the activations, synchronising, replayed as a CUDA
+ * graph when a call repeats; GPT_ERR_UNSUPPORTED with recompute, or for a
+ * head_dim that the cache does not have. */
+gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int32_t* d_prompt,
+                            const int32_t* d_prompt_len, int32_t T0, int32_t n_new, int32_t budget, int32_t recent,
+                            const int32_t* d_table_out, int32_t* d_kept, const float* d_temperature,
+                            const int32_t* d_top_k, const float* d_top_p, const float* d_min_p,
+                            const float* d_uniform, int32_t* d_out, float* d_logp, int32_t* h_evictions);
 
 /* ---------------------------------------------------------------- introspection (tests, resume) */
 

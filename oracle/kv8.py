@@ -16,9 +16,11 @@ import math
 
 import numpy as np
 
+from . import gpt_oracle as go
+
 E_MIN, E_MAX = -110, 120
 
-__all__ = ["decode", "encode", "exponent", "Cache"]
+__all__ = ["decode", "encode", "exponent", "Cache", "Decoder"]
 
 
 def _table() -> np.ndarray:
@@ -185,3 +187,81 @@ class Cache:
                     self.weight[bo, h, :len(part)] = [0.0 if slots[j] is None else src[4][slots[j][0], h, slots[j][1]]
                                                       for j in part]
         return kept
+
+
+class Decoder:
+    """A model decoding over 8-bit caches, one per layer, from prompts of different lengths: the definition that
+    gpt_generate_kv8 follows, with the tokens given by the caller.  ``noise(x)``, where given, is applied to every
+    layer's q, k, v (to see what rounding errors before the quantisation do)."""
+
+    def __init__(self, cfg, P, prompts, block_tokens, max_blocks, budget=0, recent=0, noise=None):
+        self.cfg, self.params, self.budget, self.recent = cfg, P, budget, recent
+        self.noise = noise if noise is not None else (lambda x: x)
+        B, H, hd = len(prompts), cfg.n_head, cfg.n_embd // cfg.n_head
+        self.H, self.hd, self.B = H, hd, B
+        self.capacity = max_blocks * block_tokens
+        n = 2 * B * max_blocks
+        shape = (n, H, block_tokens, hd)
+        self.tables = [np.arange(B * max_blocks).reshape(B, max_blocks), np.arange(B * max_blocks, n).reshape(B, max_blocks)]
+        self.layers = [Cache(np.zeros(shape), np.zeros(shape), np.ones((n, H)), np.ones((n, H)), self.tables[0],
+                             np.zeros(B, np.int64), np.zeros(shape[:3])) for _ in range(cfg.n_layer)]
+        self.pos = np.array([len(p) for p in prompts])
+        self.bound, self.evictions, self.kept, self.margins = int(self.pos.max()), 0, None, []
+        start = np.concatenate([[0], np.cumsum(self.pos)])
+        self.z = np.zeros((B, cfg.vocab_size))
+        qkv = [[] for _ in self.layers]
+        for b, p in enumerate(prompts):
+            _, c = go.forward(cfg, P, np.asarray(p)[None], None)
+            self.z[b] = c["z"][0, -1]
+            for l, lc in enumerate(c["layers"]):
+                qkv[l].append([self.noise(lc[x][0].transpose(1, 0, 2)) for x in "qkv"])
+        for cache, parts in zip(self.layers, qkv):
+            q, k, v = (np.concatenate([x[i] for x in parts]) for i in range(3))
+            cache.append(k, v, start)
+            if budget:
+                cache.accumulate(cache.attention(q, start, hd ** -0.5)[2])
+            cache.length = cache.length + self.pos
+
+    def step(self, tokens):
+        """Logits after one more token for each sequence."""
+        cfg, P, B = self.cfg, self.params, self.B
+        if self.budget and self.bound == self.capacity:
+            self.tables = self.tables[::-1]
+            self.kept = []
+            for cache in self.layers:
+                self.margins.append([_margin(cache, s, h, self.budget, self.recent) for s in range(B) for h in range(self.H)])
+                self.kept.append(cache.evict(self.tables[0], self.budget, self.recent))
+                cache.table, cache.length = self.tables[0], np.minimum(cache.length, self.budget)
+            self.bound = self.budget
+            self.evictions += 1
+        self.bound += 1
+        x = P["wte"][tokens] + P["wpe"][self.pos]
+        self.pos = self.pos + 1
+        start = np.arange(B + 1)
+        gpt2 = cfg.variant == "gpt2"
+        for l, cache in enumerate(self.layers):
+            pre = f"h.{l}."
+            a, _ = go._norm_fwd(cfg, x, P.get(pre + "ln_1.weight"), P.get(pre + "ln_1.bias"))
+            y = a @ P[pre + "attn.c_attn.weight"].T + (P[pre + "attn.c_attn.bias"] if gpt2 else 0.0)
+            q, k, v = (self.noise(t.reshape(B, self.H, self.hd)) for t in np.split(y, 3, axis=-1))
+            cache.append(k, v, start)
+            o, _, probs = cache.attention(q, start, self.hd ** -0.5)
+            if self.budget:
+                cache.accumulate(probs)
+            cache.length = cache.length + 1
+            x = x + o.reshape(B, -1) @ P[pre + "attn.c_proj.weight"].T + (P[pre + "attn.c_proj.bias"] if gpt2 else 0.0)
+            a, _ = go._norm_fwd(cfg, x, P.get(pre + "ln_2.weight"), P.get(pre + "ln_2.bias"))
+            h = a @ P[pre + "mlp.c_fc.weight"].T + (P[pre + "mlp.c_fc.bias"] if gpt2 else 0.0)
+            x = x + go._act_fwd(cfg, h) @ P[pre + "mlp.c_proj.weight"].T + (P[pre + "mlp.c_proj.bias"] if gpt2 else 0.0)
+        a, _ = go._norm_fwd(cfg, x, P.get("ln_f.weight"), P.get("ln_f.bias"))
+        self.z = a @ (P["wte"] if gpt2 else P["lm_head.weight"]).T
+        return self.z
+
+
+def _margin(cache, s, h, budget, recent):
+    """How far apart, relative to the larger, the lightest kept and the heaviest dropped weight are (inf: none dropped)."""
+    n = int(cache.length[s])
+    if n <= budget or recent == budget:
+        return math.inf
+    w = sorted((cache.weight[b, h, o] for b, o in cache._slots(s, n)[:n - recent]), reverse=True)
+    return (w[budget - recent - 1] - w[budget - recent]) / w[budget - recent - 1]
