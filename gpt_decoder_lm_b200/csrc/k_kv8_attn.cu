@@ -187,6 +187,82 @@ struct AttnArgs {
   float* lse;
 };
 
+// What a block has of its rows when it is done with its part of the slots.
+template <int ROWS>
+struct RowStats {
+  float m[ROWS], mv[ROWS], l[ROWS];  // maxima and sum, as above
+  float fac[8][ROWS];                // for the join: each part's factor, then the row's
+  float inv[ROWS], back[ROWS];
+};
+
+// Joins the cluster's blocks, part = [ROWS][PITCH] unnormalised outputs at each block's own maxima: block `split`
+// finishes its share of the rows' values.
+template <typename T, int HD, int ROWS, int PITCH, int THREADS>
+__device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* part, int n_split, int split, int rows,
+                                            const AttnArgs& at, int r0, int row0, int h, int heads) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int G = at.G;
+  if (n_split > 1) cl.sync(); else __syncthreads();
+  for (int r = threadIdx.x; r < rows; r += THREADS) {
+    float km[8], kv[8], kl[8], mm = -INFINITY, mmv = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const bool on = k < n_split;
+      const RowStats<ROWS>* o = n_split > 1 ? cl.map_shared_rank(&st, on ? k : 0) : &st;
+      km[k] = on ? o->m[r] : -INFINITY;
+      kv[k] = on ? o->mv[r] : -INFINITY;
+      kl[k] = on ? o->l[r] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) mm = fmaxf(mm, km[k]), mmv = fmaxf(mmv, kv[k]);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      ll += km[k] == -INFINITY ? kl[k] : kl[k] * sfu_exp2(km[k] - mm);
+      st.fac[k][r] = kv[k] == -INFINITY ? 1.f : sfu_exp2(kv[k] - mmv);
+    }
+    // a row that sees nothing: zeros, and the log of an empty sum
+    st.inv[r] = ll == 0.f ? 0.f : 1.f / ll;
+    st.back[r] = ll == 0.f ? 0.f : exp2f(mmv - mm);
+    if (split == 0 && at.lse) {
+      const int rr = row0 + r;
+      at.lse[(long)(r0 + rr / G) * heads + h * G + rr % G] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    }
+  }
+  __syncthreads();
+  T* out = reinterpret_cast<T*>(at.o);
+  const bool vec = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(at.o_ld * (long)sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
+  const int used = rows * (HD / 4), share = (used + n_split - 1) / n_split;
+  for (int i = split * share + threadIdx.x; i < min(used, (split + 1) * share); i += THREADS) {
+    const int r = i / (HD / 4), d = i % (HD / 4) * 4, rr = row0 + r;
+    float4 x[8], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (k < n_split) {
+        const float* p = part + r * PITCH + d;
+        x[k] = *reinterpret_cast<const float4*>(n_split > 1 ? cl.map_shared_rank(p, k) : p);
+      }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (k < n_split) {
+        const float f = st.fac[k][r];
+        y.x = fmaf(f, x[k].x, y.x), y.y = fmaf(f, x[k].y, y.y), y.z = fmaf(f, x[k].z, y.z), y.w = fmaf(f, x[k].w, y.w);
+      }
+    const float f = st.inv[r], b = st.back[r];
+    T v[4] = {from_f<T>(y.x * f * b), from_f<T>(y.y * f * b), from_f<T>(y.z * f * b), from_f<T>(y.w * f * b)};
+    T* p = out + (long)(r0 + rr / G) * at.o_ld + (long)(h * G + rr % G) * HD + d;
+    if (vec) {
+      if (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
+      else
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; j++) p[j] = v[j];
+    }
+  }
+  if (n_split > 1) cl.sync();  // no block leaves while another reads its shared memory
+}
+
 // One thread block (NW warps): 8 NT rows of one key / value head of one
 // sequence, over one of the cluster's equal parts of the slots.  Each warp takes
 // every NW-th tile of 32 tokens through its own ring of NS stages (cp.async, no
@@ -201,7 +277,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   constexpr int OP = HD + 4;          // pitch of a row of partial outputs
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float st_m[NW][ROWS], st_mv[NW][ROWS], st_l[NW][ROWS];
-  __shared__ float cl_m[ROWS], cl_mv[ROWS], cl_l[ROWS];
+  __shared__ RowStats<ROWS> stats;
 
   const int n_split = at.n_split, split = blockIdx.x % n_split, rt = blockIdx.x / n_split;
   const int h = blockIdx.y, s = blockIdx.z;
@@ -510,7 +586,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
       ll += st_m[i][r] == -INFINITY ? st_l[i][r] : st_l[i][r] * sfu_exp2(st_m[i][r] - mm);
       st_mv[i][r] = st_mv[i][r] == -INFINITY ? 0.f : sfu_exp2(st_mv[i][r] - mmv);  // the warp's factor
     }
-    cl_m[r] = mm, cl_mv[r] = mmv, cl_l[r] = ll;
+    stats.m[r] = mm, stats.mv[r] = mmv, stats.l[r] = ll;
   }
   __syncthreads();
   float* sum = part + NW * ROWS * OP;  // [ROWS][HD]
@@ -522,37 +598,319 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
     for (int k = 0; k < NW; k++) x = fmaf(st_mv[k][r], part[(k * ROWS + r) * OP + d], x);
     sum[i] = x;
   }
-  // ---- join the cluster's blocks: block `split` finishes its share of the rows' values
-  cg::cluster_group cl = cg::this_cluster();
-  if (n_split > 1) cl.sync(); else __syncthreads();
-  T* out = reinterpret_cast<T*>(at.o);
-  const int share = (used + n_split - 1) / n_split;
-  for (int i = split * share + threadIdx.x; i < min(used, (split + 1) * share); i += NW * 32) {
-    const int r = i / HD, d = i % HD, rr = row0 + r;
-    float mm = -INFINITY, mmv = -INFINITY, ll = 0.f, x = 0.f;
-    if (n_split == 1) {
-      mm = cl_m[r], mmv = cl_mv[r], ll = cl_l[r], x = sum[i];
-    } else {
-      for (int k = 0; k < n_split; k++) {
-        mm = fmaxf(mm, *cl.map_shared_rank(&cl_m[r], k));
-        mmv = fmaxf(mmv, *cl.map_shared_rank(&cl_mv[r], k));
-      }
-      for (int k = 0; k < n_split; k++) {
-        const float km = *cl.map_shared_rank(&cl_m[r], k), kv = *cl.map_shared_rank(&cl_mv[r], k);
-        const float kl = *cl.map_shared_rank(&cl_l[r], k), kx = *cl.map_shared_rank(&sum[i], k);
-        ll += km == -INFINITY ? kl : kl * sfu_exp2(km - mm);
-        x += kv == -INFINITY ? kx : kx * sfu_exp2(kv - mmv);
+  join_blocks<T, HD, ROWS, HD, NW * 32>(stats, sum, n_split, split, min(ROWS, R - row0), at, r0, row0, h, a.H * G);
+}
+
+// ---------------------------------------------------------------- many rows
+
+// A prompt's next part: 64 rows of one key / value head and sequence, 16 a warp,
+// over one of the cluster's equal parts of the slots.  With that many rows the
+// conversions are what costs, so a tile of codes becomes fp16 in shared memory
+// once for all warps, and the warps multiply from there (rows on the 16-row side
+// of the MMA, as S = Q K^T, O = P V).  The next tile's codes are on their way
+// meanwhile; two tiles alternate, so that one barrier a tile is enough.  The
+// statistics are those of k_kv8_attn.
+constexpr int MR = 64, MW = 4;  // rows and warps of a block
+
+template <int HD>
+__device__ __forceinline__ uint32_t half_at(int row, int chunk) {  // byte offset of 16 bytes of a tile of fp16 rows
+  const int x = HD == 32 ? (row >> 1) & 3 : row & 7;
+  return (uint32_t)(row * HD * 2 + ((chunk ^ x) << 4));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+
+template <int HD, int TK>
+struct alignas(16) HalfTile {
+  uint8_t k[TK * HD * 2];
+  uint8_t v[TK * HD * 2];
+};
+
+template <typename T, int HD, int TK, int MINB>
+__global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, AttnArgs at) {
+  constexpr int KS = HD / 16, NG = TK / 16, TERMS = sizeof(T) == 4 ? 2 : 1;
+  constexpr int CPR = HD / 16, CPT = TK * CPR / (MW * 32);  // 16-code chunks a row; of K, and of V, a thread
+  constexpr int OP = HD + 4;
+  static_assert(CPT >= 1, "a thread has a chunk");
+  extern __shared__ __align__(16) uint8_t smem[];
+  HalfTile<HD, TK>* tile_mem = reinterpret_cast<HalfTile<HD, TK>*>(smem);
+  __shared__ float g_ks[2][NG], g_v[2][NG];  // the groups' K scales and log2 V scales (-infinity: no block)
+  __shared__ RowStats<MR> stats;
+
+  const int n_split = at.n_split, split = blockIdx.x % n_split, rt = blockIdx.x / n_split;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+  int r0;
+  const int n = kv8_rows(a, s, &r0), len = kv8_len(a, s), G = at.G;
+  const int R = n * G, row0 = rt * MR;
+  if (row0 >= R) return;  // the same for every block of the cluster
+  const int cap = a.max_blocks << a.lgP;
+  const int see_lo = min(len + row0 / G + 1, cap), see_hi = min(len + min(R - 1, row0 + MR - 1) / G + 1, cap);
+  const int wrow = row0 + 16 * w;  // the warp's rows
+  const int w_lo = min(len + min(R - 1, wrow) / G + 1, cap), w_hi = min(len + min(R - 1, wrow + 15) / G + 1, cap);
+
+  const int tiles = (see_hi + TK - 1) / TK;
+  const int per = (tiles + n_split - 1) / n_split;
+  const int t0 = min(tiles, split * per), t1 = min(tiles, t0 + per);
+
+  // ---- a thread's chunks of a tile: codes in flight, their blocks looked up a tile earlier
+  int blk[CPT];
+  uint4 ck[CPT], cv[CPT];
+  float gks = 0.f, gv = -INFINITY;
+  int gblk = -1;
+  auto block_of = [&](int j) -> int {
+    if (j >= see_hi) return -1;
+    const int b = a.table[(size_t)s * a.max_blocks + (j >> a.lgP)];
+    return (unsigned)b < (unsigned)a.n_blocks ? b : -2;
+  };
+  const int trow = tid / CPR;  // the thread's first row of a tile; its others are MW * 32 / CPR apart
+  auto look = [&](int tile) {
+#pragma unroll
+    for (int u = 0; u < CPT; u++) blk[u] = tile < t1 ? block_of(tile * TK + trow + u * (MW * 32 / CPR)) : -1;
+    if (tid < NG) gblk = tile < t1 ? block_of(tile * TK + tid * 16) : -1;
+  };
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int u = 0; u < CPT; u++) {
+      ck[u] = cv[u] = make_uint4(0, 0, 0, 0);
+      if (blk[u] >= 0) {
+        const int j = tile * TK + trow + u * (MW * 32 / CPR);
+        const size_t src = ((((size_t)blk[u] * a.H + h) << a.lgP) + (j & (a.P - 1))) * HD + (tid % CPR) * 16;
+        ck[u] = *reinterpret_cast<const uint4*>(a.k + src);
+        cv[u] = *reinterpret_cast<const uint4*>(a.v + src);
       }
     }
-    // a row that sees nothing: zeros, and the log of an empty sum
-    const float y = ll == 0.f ? 0.f : x / ll * exp2f(mmv - mm);
-    const long row = r0 + rr / G;
-    const int head = h * G + rr % G;
-    out[row * at.o_ld + (long)head * HD + d] = from_f<T>(y);
-    if (d == 0 && at.lse)
-      at.lse[row * (long)(a.H * G) + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    if (tid < NG) {
+      const size_t bh = (size_t)max(gblk, 0) * a.H + h;
+      if (gblk == -2) kv8_flag(a, FLAG_BLOCK);
+      gks = gblk >= 0 ? a.ks[bh] : 0.f;
+      gv = gblk >= 0 ? (float)((int)(__float_as_uint(a.vs[bh]) >> 23) - 127) : -INFINITY;
+    }
+  };
+  // Writes the fetched tile as fp16.  A NaN that some of the rows do not see must not reach them as 0 * NaN: in a tile
+  // that not every row sees whole it is taken out of V.  True where that happened.
+  auto convert = [&](int tile, int buf) -> bool {
+    bool nan = false;
+    const bool partial = tile * TK + TK > see_lo && see_lo != see_hi;
+    HalfTile<HD, TK>& m = tile_mem[buf];
+#pragma unroll
+    for (int u = 0; u < CPT; u++) {
+      const int i = u * MW * 32 + tid, row = i / CPR, ch = 2 * (i % CPR);
+      uint32_t x[4] = {ck[u].x, ck[u].y, ck[u].z, ck[u].w}, y[4] = {cv[u].x, cv[u].y, cv[u].z, cv[u].w};
+      if (partial) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const uint32_t bad = (((y[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+          nan |= bad != 0;
+          y[j] &= ~(bad * 0xffu);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        *reinterpret_cast<uint4*>(m.k + half_at<HD>(row, ch + j)) =
+            make_uint4(f16x2_e4m3(x[2 * j]), f16x2_e4m3(x[2 * j] >> 16), f16x2_e4m3(x[2 * j + 1]), f16x2_e4m3(x[2 * j + 1] >> 16));
+        *reinterpret_cast<uint4*>(m.v + half_at<HD>(row, ch + j)) =
+            make_uint4(f16x2_e4m3(y[2 * j]), f16x2_e4m3(y[2 * j] >> 16), f16x2_e4m3(y[2 * j + 1]), f16x2_e4m3(y[2 * j + 1] >> 16));
+      }
+    }
+    if (tid < NG) g_ks[buf][tid] = gks, g_v[buf][tid] = gv;
+    return nan;
+  };
+
+  look(t0);
+  fetch(t0);
+  look(t0 + 1);
+
+  // ---- the warp's rows as the A operand: fp16 after a power of two, as in QFrag
+  uint32_t q[TERMS][KS][4];
+  float qf[2];
+  int see[2];
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    const int r = wrow + g + 8 * half;
+    const bool on = r < R;
+    see[half] = min(len + min(r, R - 1) / G + 1, cap);
+    const T* p = reinterpret_cast<const T*>(at.q) + (on ? (long)(r0 + r / G) * at.q_ld + (h * G + r % G) * HD : 0);
+    float x[KS][4], top = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        x[ks][j] = on ? to_f<T>(p[ks * 16 + 2 * t + (j & 1) + (j >> 1) * 8]) : 0.f;
+        top = fmaxf(top, fabsf(x[ks][j]));
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+    e = min(max(e, -100), 100);
+    const float up = kv8_pow2(e);
+    qf[half] = kv8_pow2(-e) * at.scale * 1.4426950408889634f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const float lo = x[ks][2 * j] * up, hi = x[ks][2 * j + 1] * up;
+        const uint32_t v = pack_f16(lo, hi);
+        q[0][ks][2 * j + half] = v;
+        if (TERMS == 2) q[TERMS - 1][ks][2 * j + half] = pack_rest(lo, hi, v);
+      }
   }
-  if (n_split > 1) cl.sync();  // no block leaves while another reads its shared memory
+  // the lane's offsets into a tile for ldmatrix; eight or sixteen rows on, they are the same but for the rows' bytes
+  uint32_t k_off[KS / 2], v_off[HD / 16];
+#pragma unroll
+  for (int ks = 0; ks < KS; ks += 2) k_off[ks / 2] = half_at<HD>(lane & 7, 2 * ks + (lane >> 3));
+#pragma unroll
+  for (int i = 0; i < HD / 8; i += 2) v_off[i / 2] = half_at<HD>(lane & 15, i + (lane >> 4));
+  float o[HD / 8][4];
+#pragma unroll
+  for (int i = 0; i < HD / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  for (int tile = t0; tile < t1; tile++) {
+    const int buf = (tile - t0) & 1;
+    const bool poison = __syncthreads_or(convert(tile, buf));
+    fetch(tile + 1);
+    look(tile + 2);
+    if (wrow >= R || tile * TK >= w_hi) continue;  // nothing that the warp's rows see
+    const uint32_t kb = (uint32_t)__cvta_generic_to_shared(tile_mem[buf].k), vb = (uint32_t)__cvta_generic_to_shared(tile_mem[buf].v);
+
+    // ---- scores: [8 tokens][row half, token parity]
+    float sc[TK / 8][4];
+#pragma unroll
+    for (int j = 0; j < TK / 8; j++) {
+      sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t b[4];
+        ldsm4(b, kb + k_off[ks / 2] + j * 16 * HD);
+#pragma unroll
+        for (int x = 0; x < TERMS; x++) {
+          mma(sc[j], q[x][ks][0], q[x][ks][1], q[x][ks][2], q[x][ks][3], b[0], b[1]);
+          mma(sc[j], q[x][ks + 1][0], q[x][ks + 1][1], q[x][ks + 1][2], q[x][ks + 1][3], b[2], b[3]);
+        }
+      }
+    }
+    float vl[NG], top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+    bool all = tile * TK + TK <= w_lo;
+#pragma unroll
+    for (int gr = 0; gr < NG; gr++) {
+      vl[gr] = g_v[buf][gr];
+      all &= vl[gr] != -INFINITY;
+      const float ks = g_ks[buf][gr];
+#pragma unroll
+      for (int x = 0; x < 2; x++)
+#pragma unroll
+        for (int y = 0; y < 4; y++) sc[2 * gr + x][y] *= qf[y >> 1] * ks;
+    }
+    if (!all) {
+#pragma unroll
+      for (int j = 0; j < TK / 8; j++)
+#pragma unroll
+        for (int y = 0; y < 4; y++)
+          if (tile * TK + 8 * j + 2 * t + (y & 1) >= see[y >> 1] || vl[j / 2] == -INFINITY) sc[j][y] = -INFINITY;
+    }
+    bool grow = false;
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+#pragma unroll
+      for (int gr = 0; gr < NG; gr++) {
+        const float x = fmaxf(fmaxf(sc[2 * gr][2 * half], sc[2 * gr][2 * half + 1]),
+                              fmaxf(sc[2 * gr + 1][2 * half], sc[2 * gr + 1][2 * half + 1]));
+        top[half] = fmaxf(top[half], x);
+        topv[half] = fmaxf(topv[half], x + vl[gr]);
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], d));
+        topv[half] = fmaxf(topv[half], __shfl_xor_sync(0xffffffffu, topv[half], d));
+      }
+      grow |= top[half] > m[half] + LAZY || topv[half] > mv[half] + LAZY;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        const float m1 = fmaxf(m[half], top[half]), mv1 = fmaxf(mv[half], topv[half]);
+        const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[half] - m1);
+        const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[half] - mv1);
+        m[half] = m1, mv[half] = mv1;
+        l[half] *= fl;
+#pragma unroll
+        for (int i = 0; i < HD / 8; i++) o[i][2 * half] *= fo, o[i][2 * half + 1] *= fo;
+      }
+    }
+    float mm[2], dv[2];
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      mm[half] = m[half] == -INFINITY ? 0.f : m[half];
+      dv[half] = mm[half] - (mv[half] == -INFINITY ? 0.f : mv[half]);
+    }
+#pragma unroll
+    for (int kk = 0; kk < NG; kk++) {
+      const float c0 = sfu_exp2(vl[kk] + dv[0]), c1 = sfu_exp2(vl[kk] + dv[1]);
+      uint32_t p[4], plo[4];
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const float e0 = sfu_exp2(sc[2 * kk + x][0] - mm[0]), e1 = sfu_exp2(sc[2 * kk + x][1] - mm[0]);
+        const float e2 = sfu_exp2(sc[2 * kk + x][2] - mm[1]), e3 = sfu_exp2(sc[2 * kk + x][3] - mm[1]);
+        l[0] += e0 + e1;
+        l[1] += e2 + e3;
+        p[2 * x] = pack_f16(e0 * c0, e1 * c0);
+        p[2 * x + 1] = pack_f16(e2 * c1, e3 * c1);
+        if (TERMS == 2) {
+          plo[2 * x] = pack_rest(e0 * c0, e1 * c0, p[2 * x]);
+          plo[2 * x + 1] = pack_rest(e2 * c1, e3 * c1, p[2 * x + 1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 8; i += 2) {
+        uint32_t b[4];
+        ldsm4t(b, vb + v_off[i / 2] + kk * 32 * HD);
+        mma(o[i], p[0], p[1], p[2], p[3], b[0], b[1]);
+        mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
+        if (TERMS == 2) {
+          mma(o[i], plo[0], plo[1], plo[2], plo[3], b[0], b[1]);
+          mma(o[i + 1], plo[0], plo[1], plo[2], plo[3], b[2], b[3]);
+        }
+      }
+    }
+    if (poison) {  // the NaN that were taken out go into the rows that see them
+      for (int row = 0; row < TK; row++) {
+        const int j = tile * TK + row, b = block_of(j);
+        if (b < 0) continue;
+        const uint8_t* c = a.v + ((((size_t)b * a.H + h) << a.lgP) + (j & (a.P - 1))) * HD;
+#pragma unroll
+        for (int i = 0; i < HD / 8; i++)
+#pragma unroll
+          for (int y = 0; y < 4; y++)
+            if ((c[8 * i + 2 * t + (y & 1)] & 0x7f) == 0x7f && j < see[y >> 1]) o[i][y] = __int_as_float(0x7fc00000);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+  }
+  __syncthreads();  // every warp is done with the tiles
+  float* part = reinterpret_cast<float*>(smem);  // [MR][OP]
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    const int r = 16 * w + g + 8 * half;
+#pragma unroll
+    for (int i = 0; i < HD / 8; i++)
+      *reinterpret_cast<float2*>(part + r * OP + 8 * i + 2 * t) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+    if (t == 0) stats.m[r] = m[half], stats.mv[r] = mv[half], stats.l[r] = l[half];
+  }
+  join_blocks<T, HD, MR, OP, MW * 32>(stats, part, n_split, split, min(MR, R - row0), at, r0, row0, h, a.H * G);
 }
 
 // ---------------------------------------------------------------- accumulation of the weights
@@ -759,24 +1117,20 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, Att
   }
 }
 
-template <typename T, int HD, int NT, int NS, int MINB>
-bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, int max_len) {
-  constexpr int NW = 4, ROWS = 8 * NT;
-  constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)(NW * ROWS * (HD + 4) + ROWS * HD) * 4;
-  const size_t smem = ring > join ? ring : join;
-  auto k = k_kv8_attn<T, HD, NT, NW, NS, MINB>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
-  // few blocks: the slots of each are split over a cluster of up to 8, each with a tile or more for every warp
-  const long row_tiles = ((long)a.max_new * at.G + ROWS - 1) / ROWS;
-  const long blocks = (long)a.S * a.H * row_tiles;
-  const long tiles = (max_len + TT - 1) / TT;
-  const long want = ((long)MINB * c.num_sms + blocks - 1) / blocks, most = (tiles + NW - 1) / NW;
-  int split = (int)(want < most ? want : most);
-  split = split < 1 ? 1 : split > 8 ? 8 : split;
+// few blocks: the slots of each are split over a cluster of up to 8, each with `least` tiles or more
+int split_of(const Ctx& c, long blocks, long resident, long tiles, long least) {
+  const long want = (resident * c.num_sms + blocks - 1) / blocks, most = (tiles + least - 1) / least;
+  const long split = want < most ? want : most;
+  return (int)(split < 1 ? 1 : split > 8 ? 8 : split);
+}
+
+template <typename K>
+bool launch_split(Ctx& c, K kernel, const Kv8Args& a, AttnArgs at, int split, long row_tiles, int threads, size_t smem) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
   at.n_split = split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split * row_tiles), a.H, a.S);
-  cfg.blockDim = dim3(NW * 32);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[1];
@@ -785,18 +1139,36 @@ bool launch_attn(Ctx& c, const Kv8Args& a, AttnArgs at, int max_len) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a, at) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kernel, a, at) == cudaSuccess;
+}
+
+template <typename T, int HD, int NT, int NS, int MINB>
+bool launch_attn(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  constexpr int NW = 4, ROWS = 8 * NT;
+  constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)(NW * ROWS * (HD + 4) + ROWS * HD) * 4;
+  const long row_tiles = ((long)a.max_new * at.G + ROWS - 1) / ROWS;
+  const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TT - 1) / TT, NW);
+  return launch_split(c, k_kv8_attn<T, HD, NT, NW, NS, MINB>, a, at, split, row_tiles, NW * 32, ring > join ? ring : join);
+}
+
+template <typename T, int HD, int TK, int MINB>
+bool launch_attn_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  constexpr size_t tiles = sizeof(HalfTile<HD, TK>) * 2, join = (size_t)MR * (HD + 4) * 4;
+  const long row_tiles = ((long)a.max_new * at.G + MR - 1) / MR;
+  const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TK - 1) / TK, 2);
+  return launch_split(c, k_kv8_attn_many<T, HD, TK, MINB>, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
 }
 
 template <typename T, int HD>
 bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long rows = (long)a.max_new * at.G;
   // Stages a warp and blocks an SM, by trial: with 64 dimensions and 8 rows two stages and five blocks took 21.3 us for
-  // 64 sequences of 12 heads, three and four 24.5 us; with 16 rows two and four 43 us for a prompt's next part, 32 rows
-  // in three and two 58 us.
+  // 64 sequences of 12 heads, three and four 24.5 us.
   constexpr int NS = HD == 32 ? 4 : 2;
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
-  return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
+  if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
+  constexpr int TK = HD == 128 && sizeof(T) == 4 ? 32 : 64;
+  return launch_attn_many<T, HD, TK, HD == 128 || sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
 }
 
 template <typename T, int HD, int NT>

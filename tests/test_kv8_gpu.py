@@ -204,6 +204,49 @@ def test_attention_many_tokens(hd, P, H, G, lens, news, dtype):
     check_attention(gpu, ref, q, q64, st, news, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,P,H,G,lens,news", [
+    (64, 16, 1, 1, [900, 0, 31], [70, 130, 17]), (128, 32, 1, 2, [300, 5], [40, 9]), (32, 64, 2, 1, [513, 64], [65, 16]),
+    (64, 128, 1, 7, [50], [19]), (128, 16, 1, 1, [1000], [129]), (32, 16, 1, 3, [7], [64])])
+def test_attention_blocks_of_rows(hd, P, H, G, lens, news, dtype):
+    """More rows than one block of the kernel takes, and fewer; with and without a split over the slots (which goes by
+    the bound on the lengths)."""
+    gpu, ref, rng = make(17, [a + b for a, b in zip(lens, news)], H, hd, P)
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), H * G, hd, dtype)
+    for max_len in (0, 1):
+        check_attention(gpu, ref, q, q64, st, news, dtype, max_len=max_len)
+    assert int(gpu.flags) == 0
+
+
+@pytest.mark.parametrize("max_len", [0, 1])
+def test_attention_blocks_of_rows_with_holes_and_nan(max_len):
+    """Block ids outside the pool, and NaN in V, among many rows; a sequence none of whose blocks is in the pool."""
+    gpu, ref, rng = make(18, [300, 90], 1, 64, 16)
+    table = ref.table.copy()
+    table[0, [0, 3, 17]] = [-1, ref.k.shape[0], 2 ** 31 - 1]
+    table[1] = -1
+    ref.table = table
+    gpu.table = torch.from_numpy(table).cuda()
+    news = [100, 90]
+    ref.length[:] = [200, 0]
+    gpu.length.copy_(torch.tensor([200, 0], dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, 190, 2, 64, "bf16")
+    out, lse, _ = check_attention(gpu, ref, q, q64, st, news, "bf16", max_len=max_len)
+    assert (out[100:] == 0).all() and torch.isneginf(lse[100:]).all() and int(gpu.flags) == gb.FLAG_BLOCK_RANGE
+    want = torch.isnan(out)
+    assert not want.any()
+    for slot, dim in ((250, 3), (170, 60)):  # the first is seen by the rows from 50 on, the second by all
+        gpu.v[int(table[0, slot // 16]), 0, slot % 16, dim] = 0xFF
+    gpu.attention(q, out, start=dev(st), max_new=100, max_len=max_len)
+    want[50:100, :, 3] = True
+    want[:100, :, 60] = True
+    assert torch.equal(torch.isnan(out), want)
+
+
 def test_attention_splits_agree_with_the_oracle():
     """One sequence, long enough to be split over a cluster's blocks; the bound on the length decides how."""
     gpu, ref, rng = make(12, [5001], 1, 64, 16)
