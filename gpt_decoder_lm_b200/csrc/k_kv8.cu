@@ -542,7 +542,6 @@ bool kv8_evict(Ctx& c, const Kv8Args& a, int hd, const int32_t* table_out, int m
   LaunchScope s(c, "kv8_move");
   const int chunks = a.P * hd / 16, wpu = chunks <= 64 ? 1 : min(chunks / 64, 8);  // 1, 2, 4 or 8
   const long units = (long)((budget + a.P - 1) / a.P) * a.H * a.S, grid = (units * wpu + MT / 32 - 1) / (MT / 32);
-  if (grid > 0x7fffffffL) return false;
   auto k = wpu == 1 ? k_kv8_move<1, 2> : wpu == 2 ? k_kv8_move<2, 2> : wpu == 4 ? k_kv8_move<4, 2>
            : chunks <= 512 ? k_kv8_move<8, 2> : k_kv8_move<8, 4>;
   k<<<(unsigned)grid, MT, 0, c.stream>>>(a, hd, table_out, max_blocks_out, budget, kept);

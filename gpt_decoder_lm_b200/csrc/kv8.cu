@@ -135,6 +135,8 @@ extern "C" gpt_status gpt_kv8_evict(const gpt_kv8_cache* cache, const int32_t* d
   if (!a.w || !d_table_out || d_table_out == cache->d_table || !d_kept || budget < 1 || recent < 0 || recent > budget ||
       max_blocks_out < 1 || (int64_t)max_blocks_out * a.P < budget)
     return GPT_ERR_INVALID_ARG;
+  // slots counted in 32 bits, and a grid of at most a block for each destination block and head
+  if (budget > (1 << 30) || (int64_t)((budget + a.P - 1) / a.P) * a.H * a.S > 0x7fffffff) return GPT_ERR_UNSUPPORTED;
   return launch(cuda_stream, [&](Ctx& c) {
     return kv8_evict(c, a, cache->head_dim, d_table_out, max_blocks_out, budget, recent, d_kept);
   });

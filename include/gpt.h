@@ -482,15 +482,17 @@ gpt_status gpt_kv8_attention(const gpt_kv8_cache* cache, const int32_t* d_start,
 
 /* Adds to each slot's weight the attention that the new tokens gave it: the sum
  * of exp(scale q k - lse) over the tokens and over the query heads that read
- * the key / value head.  Arguments as gpt_kv8_attention's, with its d_lse. */
+ * the key / value head.  Arguments as gpt_kv8_attention's, with its d_lse.  A
+ * sequence's sum for a slot is formed in a fixed order; where sequences share a
+ * block, their sums are added to the weight in no fixed order. */
 gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
                               int32_t n_head, int32_t rows_bf16, const void* d_q, int64_t q_ld, float scale,
                               int32_t max_len, const float* d_lse, void* cuda_stream);
 
 /* Eviction by accumulated weight: for every sequence and key / value head,
  * min(len, budget) slots are kept and moved, in order, into the blocks of
- * another table (d_table_out [n_seq, max_blocks_out]; the same pool, none of
- * its blocks in use by any sequence).  Of a sequence over the budget the last
+ * another table (d_table_out [n_seq, max_blocks_out]; the same pool, each of
+ * its blocks once and none in use by any sequence).  Of a sequence over the budget the last
  * `recent` slots are kept and, of the rest, the budget - recent whose weights
  * are largest (ties: the lowest slots; NaN below every number).  The heads of
  * a sequence may keep different slots.  Codes are rounded to their new block's

@@ -197,3 +197,14 @@ def test_refusals():
             call(**kw)
     assert call(n_new=40, budget=24, recent=24, table_out=other, kept=kept) > 0
     m.close()
+
+
+def test_recompute_is_refused():
+    w, over = CASES["char"]
+    m = gb.Model(gb.make_config(w.with_(precision="bf16"), recompute=1, **over), seed=1)
+    cache, _ = make_cache(oracle_config(w).with_(**over), 16, 2)
+    with pytest.raises(gb.GptError) as e:
+        m.generate_kv8(cache, torch.zeros(4, 5, dtype=torch.int32, device="cuda"), 2, torch.zeros(2, 4, device="cuda"),
+                       torch.zeros(4, 2, dtype=torch.int32, device="cuda"))
+    assert e.value.name == "GPT_ERR_UNSUPPORTED"
+    m.close()

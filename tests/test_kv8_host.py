@@ -102,3 +102,16 @@ def test_sample_rows_refusals(lib):
                dict(out=None)):
         assert call(**kw) == "GPT_ERR_INVALID_ARG", kw
     assert call(V=524289, ld=524289) == "GPT_ERR_UNSUPPORTED" and call(rows=65536) == "GPT_ERR_UNSUPPORTED"
+
+
+def test_eviction_grid_limits(lib):
+    """A budget or a number of destination blocks beyond what one launch covers is refused, not run in part."""
+    import ctypes as C
+    ptr = 1 << 20
+
+    def call(n_seq, heads, budget, blocks):
+        c = gb.Kv8CacheStruct(n_seq, heads, 64, 16, 8, 4, ptr, ptr, ptr, ptr, ptr, ptr, ptr, None)
+        return gb.STATUS[lib.gpt_kv8_evict(C.byref(c), 2 * ptr, blocks, budget, 0, ptr, None)]
+    assert call(65535, 32767, 17, 2) == "GPT_ERR_UNSUPPORTED"
+    assert call(1, 1, (1 << 30) + 16, 1 << 30) == "GPT_ERR_UNSUPPORTED"
+    assert call(1, 1, 33, 2) == "GPT_ERR_INVALID_ARG"
