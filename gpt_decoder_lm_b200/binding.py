@@ -551,30 +551,40 @@ def sample_rows(logits, uniform, out, temperature=None, top_k=None, top_p=None, 
     """gpt_sample_rows on the logits' device and its current stream: one draw per row of logits [rows, ld] (bf16 or
     fp32, contiguous rows).  uniform, temperature, top_p, min_p, logp: float32 [rows]; out, top_k: int32 [rows]."""
     import torch
-    _require(logits.dim() == 2 and logits.dtype in (torch.bfloat16, torch.float32) and logits.stride(1) == 1,
-             "sample_rows: logits are [rows, ld] of bfloat16 or float32 with contiguous rows")
-    rows, cols = logits.shape
+    kind = {torch.bfloat16: 1, torch.float32: 0}.get(logits.dtype)
+    if logits.dim() != 2 or kind is None or logits.stride(1) != 1:
+        raise GptError(1, "sample_rows: logits are [rows, ld] of bfloat16 or float32 with contiguous rows")
+    shape, dev = logits.shape, logits.get_device()
+    rows, cols = shape
     V = V or cols
-    ld = max(logits.stride(0), cols) if rows == 1 else logits.stride(0)
-    _require(V <= cols and ld >= cols, "sample_rows: more columns than the logits have, or rows that overlap")
-    ptr = []
-    for t, dtype in ((temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32), (min_p, torch.float32),
-                     (uniform, torch.float32), (out, torch.int32), (logp, torch.float32)):
+    ld = logits.stride(0)
+    if rows == 1:
+        ld = max(ld, cols)
+    if V > cols or ld < cols or dev < 0:
+        raise GptError(1, "sample_rows: more columns than the logits have, rows that overlap, or no device tensor")
+    want, f32, i32, ptr = shape[:1], torch.float32, torch.int32, []
+    for t, dtype in ((temperature, f32), (top_k, i32), (top_p, f32), (min_p, f32), (uniform, f32), (out, i32), (logp, f32)):
         if t is None:
             ptr.append(None)
-            continue
-        _require(t.dtype == dtype and t.shape == (rows,) and t.is_contiguous() and t.device == logits.device,
-                 "sample_rows: parameters are contiguous [rows] arrays (float32; top_k and out int32) on the logits' device")
-        ptr.append(t.data_ptr())
-    args = (logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, rows, V, ld, *ptr,
-            torch.cuda.current_stream(logits.device).cuda_stream)
-    if torch.cuda.current_device() != logits.device.index:
-        with torch.cuda.device(logits.device):
-            st = lib().gpt_sample_rows(*args)
+        elif t.dtype is dtype and t.shape == want and t.is_contiguous() and t.get_device() == dev:
+            ptr.append(t.data_ptr())
+        else:
+            raise GptError(1, "sample_rows: parameters are contiguous [rows] arrays (float32; top_k and out int32) on the "
+                              "logits' device")
+    _run_on(dev, lib().gpt_sample_rows, "sample_rows", logits.data_ptr(), kind, rows, V, ld, *ptr)
+
+
+def _run_on(dev: int, fn, what: str, *args):
+    """A call of the library on device dev and its current stream, which is fn's last argument."""
+    import torch
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream)
     else:
-        st = lib().gpt_sample_rows(*args)
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
     if st:
-        _check(st, None, "sample_rows")
+        _check(st, None, what)
 
 
 def _require(cond: bool, msg: str):
@@ -596,6 +606,7 @@ class KV8Cache:
         import torch
         e4m3 = torch.float8_e4m3fn
         _require(k.dim() == 4 and table.dim() == 2, "kv8: k is [blocks, heads, tokens, dim], table [sequences, blocks]")
+        _require(k.is_cuda, "kv8: the cache is in device memory")
         for t, shape, dtypes, name in ((k, k.shape, (torch.uint8, e4m3), "k"), (v, k.shape, (torch.uint8, e4m3), "v"),
                                        (k_scale, k.shape[:2], (torch.float32,), "k_scale"),
                                        (v_scale, k.shape[:2], (torch.float32,), "v_scale"),
@@ -614,6 +625,8 @@ class KV8Cache:
                                  _ptr(length), _ptr(flags))
         self._ref = C.addressof(self._c)
         self._lib = lib()
+        self._index, self._kind, self._i32, self._f32 = k.get_device(), {torch.bfloat16: 1, torch.float32: 0}, torch.int32, \
+            torch.float32
         self._table = table
 
     @classmethod
@@ -643,67 +656,63 @@ class KV8Cache:
         self._table = t
         self._c.d_table, self._c.max_blocks = _ptr(t), t.shape[1]
 
-    def _call(self, what, name, *args):
-        """The library's call on the tensors' device and its current stream."""
-        import torch
-        stream = torch.cuda.current_stream(self.device).cuda_stream
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                st = getattr(self._lib, name)(self._ref, *args, stream)
-        else:
-            st = getattr(self._lib, name)(self._ref, *args, stream)
-        if st:
-            _check(st, None, what)
-
     def _rows(self, x, heads, name):
         """Pitch and type (1: bf16) of rows [n, heads, head_dim] whose heads are contiguous."""
-        import torch
-        _require(x.dim() == 3 and (heads is None or x.shape[1] == heads) and x.shape[2] == self.head_dim and
-                 x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == self.head_dim) and
-                 x.dtype in (torch.bfloat16, torch.float32) and x.device == self.device,
-                 f"kv8: {name} is [rows, heads, head_dim] of bfloat16 or float32 with contiguous heads, on the cache's device")
-        ld = x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1] * x.shape[2])
-        _require(ld >= x.shape[1] * x.shape[2], f"kv8: the rows of {name} overlap")
-        return ld, 1 if x.dtype == torch.bfloat16 else 0
+        shape, stride, kind = x.shape, x.stride(), self._kind.get(x.dtype)
+        if len(shape) != 3 or heads is not None and shape[1] != heads or shape[2] != self.head_dim or stride[2] != 1 or \
+                shape[1] != 1 and stride[1] != self.head_dim or kind is None or x.get_device() != self._index:
+            raise GptError(1, f"kv8: {name} is [rows, heads, head_dim] of bfloat16 or float32 with contiguous heads, on the "
+                              "cache's device")
+        ld, row = stride[0], shape[1] * shape[2]
+        if ld < row:
+            if shape[0] > 1:
+                raise GptError(1, f"kv8: the rows of {name} overlap")
+            ld = row
+        return ld, kind
 
     def _start(self, start):
-        import torch
-        if start is not None:
-            _require(start.dtype == torch.int32 and tuple(start.shape) == (self.n_seq + 1,) and start.is_contiguous() and
-                     start.device == self.device, "kv8: start is int32 [n_seq + 1] on the cache's device")
-            return start.data_ptr()
-        return None
+        if start is None:
+            return None
+        if start.dtype is not self._i32 or tuple(start.shape) != (self.n_seq + 1,) or not start.is_contiguous() or \
+                start.get_device() != self._index:
+            raise GptError(1, "kv8: start is int32 [n_seq + 1] on the cache's device")
+        return start.data_ptr()
 
     def append(self, k, v, start=None, max_new=1):
         """gpt_kv8_append: k, v [rows, n_head_kv, head_dim], one type."""
         k_ld, b = self._rows(k, self.n_head_kv, "k")
-        v_ld, _ = self._rows(v, self.n_head_kv, "v")
-        _require(v.dtype == k.dtype and v.shape[0] == k.shape[0], "kv8: k and v have the same rows and type")
-        self._call("kv8_append", "gpt_kv8_append", self._start(start), k.shape[0], max_new, b, k.data_ptr(), k_ld,
-                   v.data_ptr(), v_ld)
+        v_ld, bv = self._rows(v, self.n_head_kv, "v")
+        n = k.shape[0]
+        if b != bv or v.shape[0] != n:
+            raise GptError(1, "kv8: k and v have the same rows and type")
+        _run_on(self._index, self._lib.gpt_kv8_append, "kv8_append", self._ref, self._start(start), n, max_new, b,
+                k.data_ptr(), k_ld, v.data_ptr(), v_ld)
 
     def attention(self, q, out, start=None, max_new=1, lse=None, scale=None, max_len=0):
         """gpt_kv8_attention: q, out [rows, n_head, head_dim], one type; lse (optional) float32 [rows, n_head].
         scale: 1 / sqrt(head_dim) where None."""
         q_ld, b = self._rows(q, None, "q")
-        o_ld, _ = self._rows(out, q.shape[1], "out")
-        _require(out.dtype == q.dtype and out.shape[0] == q.shape[0], "kv8: q and out have the same rows and type")
-        self._call("kv8_attention", "gpt_kv8_attention", self._start(start), q.shape[0], max_new, q.shape[1], b,
-                   q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, out.data_ptr(), o_ld,
-                   self._lse(lse, q))
+        n, heads, _ = q.shape
+        o_ld, bo = self._rows(out, heads, "out")
+        if b != bo or out.shape[0] != n:
+            raise GptError(1, "kv8: q and out have the same rows and type")
+        _run_on(self._index, self._lib.gpt_kv8_attention, "kv8_attention", self._ref, self._start(start), n, max_new, heads,
+                b, q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, out.data_ptr(), o_ld,
+                self._lse(lse, n, heads))
 
     def accumulate(self, q, lse, start=None, max_new=1, scale=None, max_len=0):
         """gpt_kv8_accumulate, with the lse that ``attention`` gave for q."""
         q_ld, b = self._rows(q, None, "q")
-        self._call("kv8_accumulate", "gpt_kv8_accumulate", self._start(start), q.shape[0], max_new, q.shape[1], b,
-                   q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, self._lse(lse, q))
+        n, heads, _ = q.shape
+        _run_on(self._index, self._lib.gpt_kv8_accumulate, "kv8_accumulate", self._ref, self._start(start), n, max_new, heads,
+                b, q.data_ptr(), q_ld, self.head_dim ** -0.5 if scale is None else scale, max_len, self._lse(lse, n, heads))
 
-    def _lse(self, lse, q):
-        import torch
+    def _lse(self, lse, n, heads):
         if lse is None:
             return None
-        _require(lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous() and
-                 lse.device == self.device, "kv8: lse is float32 [rows, n_head], contiguous, on the cache's device")
+        if lse.dtype is not self._f32 or tuple(lse.shape) != (n, heads) or not lse.is_contiguous() or \
+                lse.get_device() != self._index:
+            raise GptError(1, "kv8: lse is float32 [rows, n_head], contiguous, on the cache's device")
         return lse.data_ptr()
 
     def evict(self, table_out, budget: int, recent: int, kept):
@@ -715,13 +724,13 @@ class KV8Cache:
                  "kv8: table_out is int32 [n_seq, blocks] on the cache's device")
         _require(kept.dtype == torch.int32 and tuple(kept.shape) == (self.n_seq, self.n_head_kv, budget) and
                  kept.is_contiguous() and kept.device == self.device, "kv8: kept is int32 [n_seq, n_head_kv, budget]")
-        self._call("kv8_evict", "gpt_kv8_evict", table_out.data_ptr(), table_out.shape[1], budget, recent,
-                   kept.data_ptr())
+        _run_on(self._index, self._lib.gpt_kv8_evict, "kv8_evict", self._ref, table_out.data_ptr(), table_out.shape[1],
+                budget, recent, kept.data_ptr())
 
     def advance(self, start=None, n_rows=None, max_new=1, max_len=0):
         """gpt_kv8_advance: the lengths grow by the step's rows (n_rows: one for each sequence where None)."""
-        self._call("kv8_advance", "gpt_kv8_advance", self._start(start), self.n_seq if n_rows is None else n_rows,
-                   max_new, max_len)
+        _run_on(self._index, self._lib.gpt_kv8_advance, "kv8_advance", self._ref, self._start(start),
+                self.n_seq if n_rows is None else n_rows, max_new, max_len)
 
 
 def test_gemm(backend, M, N, K, A, lda, a_kmajor, B, ldb, b_kmajor, epi_kind, act=0, out=None, out2=None, ldo=0,

@@ -525,7 +525,8 @@ bool kv8_evict(Ctx& c, const Kv8Args& a, int hd, const int32_t* table_out, int m
     const int threads = nb > 1 ? 512 : 256;
     auto k = nb > 1 ? (fits ? k_kv8_select<512, true> : k_kv8_select<512, false>)
                     : (fits ? k_kv8_select<256, true> : k_kv8_select<256, false>);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, EKEYS * 4) != cudaSuccess) return false;
+    if (fits && !(nb > 1 ? allow_smem<k_kv8_select<512, true>>(EKEYS * 4) : allow_smem<k_kv8_select<256, true>>(EKEYS * 4)))
+      return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(nb, a.H, a.S);
     cfg.blockDim = dim3(threads);

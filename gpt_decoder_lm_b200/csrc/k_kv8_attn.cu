@@ -1124,9 +1124,9 @@ int split_of(const Ctx& c, long blocks, long resident, long tiles, long least) {
   return (int)(split < 1 ? 1 : split > 8 ? 8 : split);
 }
 
-template <typename K>
-bool launch_split(Ctx& c, K kernel, const Kv8Args& a, AttnArgs at, int split, long row_tiles, int threads, size_t smem) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+template <auto Kernel>
+bool launch_split(Ctx& c, const Kv8Args& a, AttnArgs at, int split, long row_tiles, int threads, size_t smem) {
+  if (!allow_smem<Kernel>((int)smem)) return false;
   at.n_split = split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split * row_tiles), a.H, a.S);
@@ -1139,7 +1139,7 @@ bool launch_split(Ctx& c, K kernel, const Kv8Args& a, AttnArgs at, int split, lo
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, at) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, Kernel, a, at) == cudaSuccess;
 }
 
 template <typename T, int HD, int NT, int NS, int MINB>
@@ -1148,7 +1148,7 @@ bool launch_attn(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)(NW * ROWS * (HD + 4) + ROWS * HD) * 4;
   const long row_tiles = ((long)a.max_new * at.G + ROWS - 1) / ROWS;
   const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TT - 1) / TT, NW);
-  return launch_split(c, k_kv8_attn<T, HD, NT, NW, NS, MINB>, a, at, split, row_tiles, NW * 32, ring > join ? ring : join);
+  return launch_split<k_kv8_attn<T, HD, NT, NW, NS, MINB>>(c, a, at, split, row_tiles, NW * 32, ring > join ? ring : join);
 }
 
 template <typename T, int HD, int TK, int MINB>
@@ -1156,7 +1156,7 @@ bool launch_attn_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   constexpr size_t tiles = sizeof(HalfTile<HD, TK>) * 2, join = (size_t)MR * (HD + 4) * 4;
   const long row_tiles = ((long)a.max_new * at.G + MR - 1) / MR;
   const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TK - 1) / TK, 2);
-  return launch_split(c, k_kv8_attn_many<T, HD, TK, MINB>, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
+  return launch_split<k_kv8_attn_many<T, HD, TK, MINB>>(c, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
 }
 
 template <typename T, int HD>

@@ -677,7 +677,8 @@ bool launch(Ctx& c, RowArgs a, int rows) {
   const bool fits = bytes(nb) <= SMEM_ROW;
   auto k = fits ? k_sample_rows<T, true> : k_sample_rows<T, false>;
   const size_t smem = (nb > 1 ? HEAD_MANY : HEAD_ONE) + (fits ? (size_t)bytes(nb) : 0);
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, HEAD_MANY + SMEM_ROW) != cudaSuccess) return false;
+  constexpr int most = HEAD_MANY + SMEM_ROW;
+  if (!(fits ? allow_smem<k_sample_rows<T, true>>(most) : allow_smem<k_sample_rows<T, false>>(most))) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nb, rows);
   cfg.blockDim = dim3(NT);

@@ -1,6 +1,8 @@
 // Internal launch interface between the step engine and the kernels.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gpt {
@@ -15,6 +17,20 @@ struct Ctx {
   uint64_t launches = 0;
   Timing* timing = nullptr;   // null when timing is off
 };
+
+// Lets kernel K have `bytes` of dynamic shared memory a block on the current device: asked of the driver once for each
+// device, not at every launch.
+template <auto K>
+bool allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
 
 void timing_begin(Ctx& c, const char* name);
 void timing_end(Ctx& c, const char* name);
