@@ -16,10 +16,10 @@
 // searched by their keys' digits with exact counts or masses.  Rows whose
 // tokens crowd into a bin are searched in place.
 //
-// Measured on a B200, 50,257 logits: one row 4.5 us greedy, 8 us with min-p,
-// 18 us with top-k or top-p (latency: four or five cluster barriers and the
-// passes between them); 256 bf16 rows 9 us greedy (42% of the copy bandwidth),
-// 38 us unfiltered (the weights' fp64 arithmetic: 13 operations a token), 58 us
+// Measured on a B200, 50,257 logits: one row 4 us greedy, 7 us with min-p, 14
+// to 17 us with top-k or top-p (latency: four or five cluster barriers and the
+// passes between them); 256 bf16 rows 9 us greedy (43% of the copy bandwidth),
+// 38 us unfiltered (the weights' fp64 arithmetic: 13 operations a token), 57 us
 // nucleus (beside that, one shared-memory addition a token: about five cycles
 // a warp).
 #include <cfloat>
@@ -121,15 +121,17 @@ __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 }
 
 // Reductions over the block's threads and the cluster's blocks.  Slots
-// alternate, so that one barrier an exchange is enough.
+// alternate, so that one barrier an exchange is enough.  A block writes its
+// value into every block's memory before the barrier: behind it all reads are
+// local, and no block waits for another before it leaves.
 struct Exchange {
   u64 warp[2][NWP];
-  u64 block[2];
+  u64 block[2][8];
 };
 struct Group {
   cg::cluster_group cl;
   Exchange& x;
-  int nb, turn;
+  int nb, rank, turn, block_turn;
   __device__ __forceinline__ void sync() {
     if (nb > 1) cl.sync(); else __syncthreads();
   }
@@ -144,9 +146,10 @@ struct Group {
     __syncthreads();
     v = warp(lane < NWP ? x.warp[turn][lane] : 0ull);
     if (alone || nb == 1) return v;
-    if (threadIdx.x == 0) x.block[turn] = v;
+    block_turn ^= 1;
+    if (threadIdx.x < nb) *cl.map_shared_rank(&x.block[block_turn][rank], threadIdx.x) = v;
     cl.sync();
-    return warp(lane < nb ? *cl.map_shared_rank(&x.block[turn], lane) : 0ull);
+    return warp(lane < nb ? x.block[block_turn][lane] : 0ull);
   }
   __device__ u64 sum(u64 v) { return reduce<false>(v, false); }
   __device__ uint32_t top(uint32_t v) { return (uint32_t)reduce<true>(v, false); }
@@ -269,7 +272,8 @@ struct Shared {
   Exchange x;
   u64 wmass[NWP];       // kept mass of each warp's positions
   u64 sums[2][NWP];     // each warp's share of: all that is counted, what lies above the listed tokens
-  int n_list;           // tokens that the block has listed (or would have)
+  u64 row[3][8];        // each block's: the same two, and the tokens that it has listed (or would have)
+  int n_list;           // tokens that the block lists
   uint32_t late[3 * NWP];  // the kept listed tokens' share of wmass, 15 bits at a time
   double wsum[NWP];
   int pick[2];
@@ -284,7 +288,8 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int nb = gridDim.x, rank = blockIdx.x, row = blockIdx.y;
-  Group grp{cg::this_cluster(), sh.x, nb, 0};
+  Group grp{cg::this_cluster(), sh.x, nb, rank, 0, 0};
+  if (nb > 1) grp.cl.barrier_arrive();  // another block's memory may be written once all have started
   const int i0 = min(a.V, rank * a.seg);
   Part<T, SMEM> part;
   part.g = reinterpret_cast<const T*>(a.logits) + (long)row * a.ld + i0;
@@ -304,7 +309,9 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
   const float temp = a.temperature ? a.temperature[row] : 1.f;
   const int k = a.top_k ? a.top_k[row] : 0;
   const float tp = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.uniform[row];
-  float top = key_logit<T>(grp.top(logit_key<T>(part.load(positions))));
+  const float mine_top = part.load(positions);
+  if (nb > 1) grp.cl.barrier_wait();
+  float top = key_logit<T>(grp.top(logit_key<T>(mine_top)));
   if (top == -INFINITY || !(temp > 0.f)) {
     // nothing to draw from, or greedy: the lowest index of the largest logit
     uint32_t best = 0;
@@ -319,7 +326,6 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
       a.out[row] = top == -INFINITY ? -1 : (int)~best;
       if (a.logp) a.logp[row] = top == -INFINITY ? -INFINITY : 0.f;
     }
-    if (nb > 1) grp.sync();  // no block leaves while another reads its shared memory
     return;
   }
   if (top == INFINITY) {
@@ -462,6 +468,17 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
     all = warp_sum_u64(all);
     above = warp_sum_u64(above);
     if (lane == 0) sh.sums[0][w] = all, sh.sums[1][w] = above;
+    __syncthreads();
+    if (w == 0) {
+      all = warp_sum_u64(lane < NWP ? sh.sums[0][lane] : 0ull);
+      above = warp_sum_u64(lane < NWP ? sh.sums[1][lane] : 0ull);
+      if (lane < nb) {
+        u64* to = nb > 1 ? grp.cl.map_shared_rank(&sh.row[0][rank], lane) : &sh.row[0][0];
+        to[0] = all;
+        to[8] = above;
+        to[16] = sh.n_list;
+      }
+    }
     grp.sync();  // the lists, their lengths and sums; the histogram has been read by all
     // ---- the row's listed tokens, two a thread, and the row's sums
     bool in_list;  // else too many: they are searched in place
@@ -469,19 +486,10 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
     uint32_t e[GATHER / NT];
     u64 hold[GATHER / NT];
     bool own[GATHER / NT];
-    all = above = 0;
     {
-      const int c = lane < nb ? nb > 1 ? *grp.cl.map_shared_rank(&sh.n_list, lane) : sh.n_list : 0;
-#pragma unroll
-      for (int i = 0; i < 8 * NWP / 32; i++) {
-        const int x = 32 * i + lane;
-        if (x < nb * NWP) {
-          const u64* p = &sh.sums[0][x % NWP];
-          if (nb > 1) p = grp.cl.map_shared_rank(p, x / NWP);
-          all += p[0];
-          above += p[NWP];
-        }
-      }
+      const int c = lane < nb ? (int)sh.row[2][lane] : 0;
+      all = warp_sum_u64(lane < nb ? sh.row[0][lane] : 0ull);
+      above = warp_sum_u64(lane < nb ? sh.row[1][lane] : 0ull);
       n_list = __reduce_add_sync(0xffffffffu, c);
       in_list = n_list <= GATHER;
 #pragma unroll
@@ -500,8 +508,6 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
         }
       }
     }
-    all = warp_sum_u64(all);
-    above = warp_sum_u64(above);
     // ---- The largest key at which `above` and what the tokens between hold at or above the key reach the need: nine
     // bits at a time, by a histogram of the tokens that share the bits found so far.  Its 44-bit sums are kept as three
     // of 15 bits.
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
   const u64 mass = grp.sum(lane == 0 ? mine : 0ull);
   u64 before = 0;
   if (nb > 1)
-    for (int i = 0; i < rank; i++) before += *grp.cl.map_shared_rank(&sh.x.block[grp.turn], i);
+    for (int i = 0; i < rank; i++) before += sh.x.block[grp.block_turn][i];
   u64 target = u > 0.f ? (u64)((double)u * (double)mass) : 0ull;
   target = min(target, mass - 1);
   int cw = -1;  // the warp whose positions hold the token
@@ -662,7 +668,6 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
       }
     }
   }
-  if (nb > 1) grp.sync();
 }
 
 template <typename T>
