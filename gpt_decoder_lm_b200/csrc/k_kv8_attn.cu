@@ -312,14 +312,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   const int t0 = min(tiles, split * per), t1 = min(tiles, t0 + per);
   Stage<HD>* ring = reinterpret_cast<Stage<HD>*>(smem) + w * NS;
 
-  // block ids of the next tile to be requested, looked up one tile ahead
+  // block ids of the next tile to be requested, looked up one tile ahead and first touched when they are needed
   int b0 = -1, b1 = -1;
   auto look = [&](int tile) {
     b0 = b1 = -1;
     if (tile < t1) {
-      b0 = kv8_block(a, s, (tile * TT) >> a.lgP);
-      const int j1 = (tile * TT + 16) >> a.lgP;
-      b1 = tile * TT + 16 < see_hi ? (j1 == (tile * TT) >> a.lgP ? b0 : kv8_block(a, s, j1)) : -1;
+      const int32_t* ids = a.table + (size_t)s * a.max_blocks;
+      b0 = ids[(tile * TT) >> a.lgP];
+      if (tile * TT + 16 < see_hi) b1 = ids[(tile * TT + 16) >> a.lgP];
     }
   };
   // A group's 16 rows are contiguous in its block: chunk u of a tile lies 512 u bytes on, in memory and (but for
@@ -331,6 +331,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
     if (tile < t1) {
       Stage<HD>& st = ring[slot];
       const int base = tile * TT;
+      const bool bad0 = (unsigned)b0 >= (unsigned)a.n_blocks, bad1 = (unsigned)b1 >= (unsigned)a.n_blocks;
+      if (bad0 || bad1) {
+        if (lane == 0 && (bad0 || base + 16 < see_hi)) kv8_flag(a, FLAG_BLOCK);
+        if (bad0) b0 = -1;
+        if (bad1) b1 = -1;
+      }
       const size_t p0 = ((size_t)max(b0, 0) * a.H + h), p1 = ((size_t)max(b1, 0) * a.H + h);
       const size_t s0 = ((p0 << a.lgP) + (base & (a.P - 1))) * HD + lane * 16;
       const size_t s1 = ((p1 << a.lgP) + ((base + 16) & (a.P - 1))) * HD + lane * 16;
@@ -664,35 +670,37 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   // ---- a thread's chunks of a tile: codes in flight, their blocks looked up a tile earlier
   int blk[CPT];
   uint4 ck[CPT], cv[CPT];
-  float gks = 0.f, gv = -INFINITY;
+  float gks = 0.f, gvs = 0.f;  // 0: no block
   int gblk = -1;
-  auto block_of = [&](int j) -> int {
-    if (j >= see_hi) return -1;
-    const int b = a.table[(size_t)s * a.max_blocks + (j >> a.lgP)];
-    return (unsigned)b < (unsigned)a.n_blocks ? b : -2;
-  };
+  const int32_t* ids = a.table + (size_t)s * a.max_blocks;
   const int trow = tid / CPR;  // the thread's first row of a tile; its others are MW * 32 / CPR apart
   auto look = [&](int tile) {
 #pragma unroll
-    for (int u = 0; u < CPT; u++) blk[u] = tile < t1 ? block_of(tile * TK + trow + u * (MW * 32 / CPR)) : -1;
-    if (tid < NG) gblk = tile < t1 ? block_of(tile * TK + tid * 16) : -1;
+    for (int u = 0; u < CPT; u++) {
+      const int j = tile * TK + trow + u * (MW * 32 / CPR);
+      blk[u] = -1;
+      if (tile < t1 && j < see_hi) blk[u] = ids[j >> a.lgP];  // first touched when the tile is fetched
+    }
+    gblk = -1;
+    if (tid < NG && tile < t1 && tile * TK + tid * 16 < see_hi) gblk = ids[(tile * TK + tid * 16) >> a.lgP];
   };
   auto fetch = [&](int tile) {
 #pragma unroll
     for (int u = 0; u < CPT; u++) {
       ck[u] = cv[u] = make_uint4(0, 0, 0, 0);
-      if (blk[u] >= 0) {
+      if ((unsigned)blk[u] < (unsigned)a.n_blocks) {
         const int j = tile * TK + trow + u * (MW * 32 / CPR);
         const size_t src = ((((size_t)blk[u] * a.H + h) << a.lgP) + (j & (a.P - 1))) * HD + (tid % CPR) * 16;
         ck[u] = *reinterpret_cast<const uint4*>(a.k + src);
         cv[u] = *reinterpret_cast<const uint4*>(a.v + src);
       }
     }
-    if (tid < NG) {
-      const size_t bh = (size_t)max(gblk, 0) * a.H + h;
-      if (gblk == -2) kv8_flag(a, FLAG_BLOCK);
-      gks = gblk >= 0 ? a.ks[bh] : 0.f;
-      gv = gblk >= 0 ? (float)((int)(__float_as_uint(a.vs[bh]) >> 23) - 127) : -INFINITY;
+    if (tid < NG && tile < t1) {
+      const bool on = (unsigned)gblk < (unsigned)a.n_blocks;
+      if (!on && tile * TK + tid * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
+      const size_t bh = (size_t)(on ? gblk : 0) * a.H + h;
+      gks = gvs = 0.f;
+      if (on) gks = a.ks[bh], gvs = a.vs[bh];
     }
   };
   // Writes the fetched tile as fp16.  A NaN that some of the rows do not see must not reach them as 0 * NaN: in a tile
@@ -721,7 +729,10 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
             make_uint4(f16x2_e4m3(y[2 * j]), f16x2_e4m3(y[2 * j] >> 16), f16x2_e4m3(y[2 * j + 1]), f16x2_e4m3(y[2 * j + 1] >> 16));
       }
     }
-    if (tid < NG) g_ks[buf][tid] = gks, g_v[buf][tid] = gv;
+    if (tid < NG) {
+      g_ks[buf][tid] = gks;
+      g_v[buf][tid] = gvs > 0.f ? (float)((int)(__float_as_uint(gvs) >> 23) - 127) : -INFINITY;
+    }
     return nan;
   };
 
@@ -883,8 +894,10 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     }
     if (poison) {  // the NaN that were taken out go into the rows that see them
       for (int row = 0; row < TK; row++) {
-        const int j = tile * TK + row, b = block_of(j);
-        if (b < 0) continue;
+        const int j = tile * TK + row;
+        if (j >= see_hi) break;
+        const int b = ids[j >> a.lgP];
+        if ((unsigned)b >= (unsigned)a.n_blocks) continue;
         const uint8_t* c = a.v + ((((size_t)b * a.H + h) << a.lgP) + (j & (a.P - 1))) * HD;
 #pragma unroll
         for (int i = 0; i < HD / 8; i++)
@@ -1026,20 +1039,21 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, Att
 #pragma unroll
     for (int gr = 0; gr < 2; gr++) {
       const int j = tile * TT + gr * 16;
-      b[gr] = j < see_hi ? a.table[(size_t)s * a.max_blocks + (j >> a.lgP)] : -1;
-      if (j < see_hi && (unsigned)b[gr] >= (unsigned)a.n_blocks) b[gr] = -2;
+      b[gr] = -1;
+      if (j < see_hi) b[gr] = a.table[(size_t)s * a.max_blocks + (j >> a.lgP)];  // first touched when it is fetched
     }
   };
   auto fetch = [&](int tile, const int (&b)[2], uint32_t (&kw)[2][2][KS], float (&ks)[2]) {
 #pragma unroll
     for (int gr = 0; gr < 2; gr++) {
-      const size_t bh = (size_t)max(b[gr], 0) * a.H + h;
-      ks[gr] = b[gr] >= 0 ? a.ks[bh] : 0.f;
+      const bool there = (unsigned)b[gr] < (unsigned)a.n_blocks;
+      const size_t bh = (size_t)(there ? b[gr] : 0) * a.H + h;
+      ks[gr] = there ? a.ks[bh] : 0.f;
 #pragma unroll
       for (int half = 0; half < 2; half++) {
         const int j = tile * TT + gr * 16 + key_token(g, half);
         const uint8_t* p = a.k + ((bh << a.lgP) + (j & (a.P - 1))) * HD;
-        const bool on = b[gr] >= 0 && j < see_hi;
+        const bool on = there && j < see_hi;
         if (HD == 32) {
           const uint2 c = on ? *reinterpret_cast<const uint2*>(p + t * 8) : make_uint2(0, 0);
           kw[gr][half][0] = c.x, kw[gr][half][1] = c.y;
@@ -1100,10 +1114,11 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, Att
         sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
         sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
       }
-      if (now[gr] == -2 && lane == 0) kv8_flag(a, FLAG_BLOCK);
+      const bool there = (unsigned)now[gr] < (unsigned)a.n_blocks;
+      if (!there && lane == 0 && tile * TT + gr * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
       // one of the four lanes that hold a sum adds it (atomically: two sequences may share a block)
       const int j = tile * TT + gr * 16 + key_token(g, t & 1);
-      if (t < 2 && j < see_hi && now[gr] >= 0)
+      if (t < 2 && j < see_hi && there)
         atomicAdd(a.w + ((((size_t)now[gr] * a.H + h) << a.lgP) + (j & (a.P - 1))), t ? sum[1] : sum[0]);
     }
 #pragma unroll
