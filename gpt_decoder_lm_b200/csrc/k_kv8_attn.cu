@@ -231,33 +231,40 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
   __syncthreads();
   T* out = reinterpret_cast<T*>(at.o);
   const bool vec = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(at.o_ld * (long)sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
-  const int used = rows * (HD / 4), share = (used + n_split - 1) / n_split;
-  for (int i = split * share + threadIdx.x; i < min(used, (split + 1) * share); i += THREADS) {
-    const int r = i / (HD / 4), d = i % (HD / 4) * 4, rr = row0 + r;
-    float4 x[8], y = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = ROWS * HD / 4 >= 4 * THREADS ? 4 : 1;  // values in flight a thread, of each block
+  const int used = rows * (HD / 4), share = (used + n_split - 1) / n_split, end = min(used, (split + 1) * share);
+  for (int i0 = split * share + threadIdx.x; i0 < end; i0 += U * THREADS) {
+    float4 y[U];
 #pragma unroll
-    for (int k = 0; k < 8; k++)
-      if (k < n_split) {
-        const float* p = part + r * PITCH + d;
-        x[k] = *reinterpret_cast<const float4*>(n_split > 1 ? cl.map_shared_rank(p, k) : p);
-      }
+    for (int u = 0; u < U; u++) y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < n_split; k++) {
+      const float* from = n_split > 1 ? cl.map_shared_rank(part, k) : part;
 #pragma unroll
-    for (int k = 0; k < 8; k++)
-      if (k < n_split) {
+      for (int u = 0; u < U; u++) {
+        const int i = min(i0 + u * THREADS, end - 1), r = i / (HD / 4);
+        const float4 x = *reinterpret_cast<const float4*>(from + r * PITCH + i % (HD / 4) * 4);
         const float f = st.fac[k][r];
-        y.x = fmaf(f, x[k].x, y.x), y.y = fmaf(f, x[k].y, y.y), y.z = fmaf(f, x[k].z, y.z), y.w = fmaf(f, x[k].w, y.w);
+        y[u].x = fmaf(f, x.x, y[u].x), y[u].y = fmaf(f, x.y, y[u].y), y[u].z = fmaf(f, x.z, y[u].z), y[u].w = fmaf(f, x.w, y[u].w);
       }
-    const float f = st.inv[r], b = st.back[r];
-    T v[4] = {from_f<T>(y.x * f * b), from_f<T>(y.y * f * b), from_f<T>(y.z * f * b), from_f<T>(y.w * f * b)};
-    T* p = out + (long)(r0 + rr / G) * at.o_ld + (long)(h * G + rr % G) * HD + d;
-    if (vec) {
-      if (sizeof(T) == 2)
-        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
-      else
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(v);
-    } else {
+    }
 #pragma unroll
-      for (int j = 0; j < 4; j++) p[j] = v[j];
+    for (int u = 0; u < U; u++) {
+      const int i = i0 + u * THREADS;
+      if (i >= end) break;
+      const int r = i / (HD / 4), rr = row0 + r;
+      const float f = st.inv[r], b = st.back[r];
+      T v[4] = {from_f<T>(y[u].x * f * b), from_f<T>(y[u].y * f * b), from_f<T>(y[u].z * f * b), from_f<T>(y[u].w * f * b)};
+      T* p = out + (long)(r0 + rr / G) * at.o_ld + (long)(h * G + rr % G) * HD + i % (HD / 4) * 4;
+      if (vec) {
+        if (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
+        else
+          *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) p[j] = v[j];
+      }
     }
   }
   if (n_split > 1) cl.sync();  // no block leaves while another reads its shared memory
@@ -736,26 +743,38 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     return nan;
   };
 
+  // ---- the warp's rows, asked for before the first tile whose block ids are still on their way
   look(t0);
+  T qraw[2][KS][4];
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    const int r = wrow + g + 8 * half;
+    const T* p = reinterpret_cast<const T*>(at.q) + (r < R ? (long)(r0 + r / G) * at.q_ld + (h * G + r % G) * HD : 0);
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        qraw[half][ks][j] = from_f<T>(0.f);
+        if (r < R) qraw[half][ks][j] = p[ks * 16 + 2 * t + (j & 1) + (j >> 1) * 8];
+      }
+  }
   fetch(t0);
   look(t0 + 1);
 
-  // ---- the warp's rows as the A operand: fp16 after a power of two, as in QFrag
+  // ---- the A operand: fp16 after a power of two, as in QFrag
   uint32_t q[TERMS][KS][4];
   float qf[2];
   int see[2];
 #pragma unroll
   for (int half = 0; half < 2; half++) {
     const int r = wrow + g + 8 * half;
-    const bool on = r < R;
     see[half] = min(len + min(r, R - 1) / G + 1, cap);
-    const T* p = reinterpret_cast<const T*>(at.q) + (on ? (long)(r0 + r / G) * at.q_ld + (h * G + r % G) * HD : 0);
     float x[KS][4], top = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ks++)
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        x[ks][j] = on ? to_f<T>(p[ks * 16 + 2 * t + (j & 1) + (j >> 1) * 8]) : 0.f;
+        x[ks][j] = to_f<T>(qraw[half][ks][j]);
         top = fmaxf(top, fabsf(x[ks][j]));
       }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
