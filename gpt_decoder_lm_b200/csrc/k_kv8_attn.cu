@@ -1214,10 +1214,10 @@ void launch_accumulate(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len
 template <typename T, int HD, int NT>
 void launch_accumulate_few(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   constexpr int MINB = HD == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 6 : 4;
-  // a warp for every two tiles, or as many blocks as the GPU holds
+  // a warp for every two tiles, but no more blocks than the GPU holds at once
   const long tiles = (max_len + TT - 1) / TT, most = (tiles + 7) / 8, pairs = (long)a.H * a.S;
-  long split = ((long)MINB * c.num_sms + pairs - 1) / pairs;
-  split = split > most ? most : split;
+  long split = (long)MINB * c.num_sms / pairs;
+  split = split > most ? most : split < 1 ? 1 : split;
   k_kv8_accumulate_few<T, HD, NT, MINB><<<dim3((unsigned)split, a.H, a.S), 128, 0, c.stream>>>(a, at);
 }
 template <typename T, int HD>
