@@ -42,7 +42,8 @@ __device__ __forceinline__ void kv8_flag(const Kv8Args& a, uint32_t bit) {
 // [0, n_rows] or give a sequence more than max_new count as no tokens.
 __device__ __forceinline__ int kv8_rows(const Kv8Args& a, int s, int* r0) {
   if (a.every) {
-    const int i = s % a.n_count;
+    int i = s;
+    while (i >= a.n_count) i -= a.n_count;  // (a division would cost the other callers registers)
     *r0 = i * a.every;
     return min(max(a.count[i], 0), a.max_new);
   }
