@@ -1083,8 +1083,7 @@ bool kv8_layer(gpt_model* m, const Kv8Args& a, const T* qkv, T* o, int max_len, 
   const float scale = 1.0f / sqrtf((float)m->hd);
   kv8_append(c, a, m->hd, b16, qkv + d, 3 * d, qkv + 2 * d, 3 * d);
   if (o && !kv8_attention(c, a, m->hd, 1, b16, qkv, 3 * d, scale, max_len, o, d, weights ? m->lse : nullptr)) return false;
-  if (weights) kv8_accumulate(c, a, m->hd, 1, b16, qkv, 3 * d, scale, max_len, m->lse);
-  return true;
+  return !weights || kv8_accumulate(c, a, m->hd, 1, b16, qkv, 3 * d, scale, max_len, m->lse);
 }
 
 // ============================================================================

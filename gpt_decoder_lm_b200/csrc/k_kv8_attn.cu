@@ -949,94 +949,187 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 
 // weight[slot] += sum over the rows of exp(score - lse): the QK product again,
 // now with the rows' final statistics, so that a slot's sum is formed by one
-// warp in a fixed order.  Here a warp holds the codes of TW tiles in registers
-// and takes all rows past them; k_kv8_accumulate_few has the rows in registers.
-template <typename T, int HD, int NT, int TW>
-__global__ void __launch_bounds__(256) k_kv8_accumulate(Kv8Args a, AttnArgs at) {
-  constexpr int ROWS = 8 * NT, KS = HD / 16;
+// warp in a fixed order.  Here (many rows) a warp holds the codes of 32 slots as
+// the product's 16-row operand, converted once, and all rows pass by: 64 at a
+// time as fp16 in shared memory, made once for the block's four warps while the
+// tile before is used.  k_kv8_accumulate_few has the rows in registers.
+constexpr int AR = 64, AT = 128;  // rows a tile, slots a block
+
+// Where dimension d of a row lies so that the 16 x 8 x 16 MMA, which takes a row's halves in order, meets the
+// dimensions that a lane's codes have (QFrag::dim0)
+template <int HD>
+__device__ __forceinline__ constexpr int half_place(int d) {
+  const int t = HD == 32 ? d / 8 : d % 64 / 16, ks = HD == 32 ? d % 8 / 4 : d / 64 * 4 + d % 16 / 4, j = d % 4;
+  return ks * 16 + 2 * t + (j & 1) + (j >> 1) * 8;
+}
+
+template <typename T, int HD, int MINB>
+__global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_many(Kv8Args a, AttnArgs at) {
+  constexpr int KS = HD / 16, TERMS = sizeof(T) == 4 ? 2 : 1, DPT = HD / 2;  // dimensions of a row that a thread brings
+  constexpr int TILE = AR * HD * 2;
+  extern __shared__ __align__(16) uint8_t smem[];  // [2][TERMS][AR][HD] fp16
+  __shared__ float r_f[2][AR], r_ls[2][AR];
+  __shared__ int r_see[2][AR];
   const int h = blockIdx.y, s = blockIdx.z;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
   int r0;
   const int n = kv8_rows(a, s, &r0), len = kv8_len(a, s), G = at.G, R = n * G;
   const int cap = a.max_blocks << a.lgP, see_hi = min(len + n, cap);
   if (n == 0) return;
+  const T* qs = reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + (long)h * G * HD;
+  const bool vec = ((reinterpret_cast<uintptr_t>(qs) | (uintptr_t)(at.q_ld * (long)sizeof(T))) & 15) == 0;
+  // the lane's offsets into a tile for ldmatrix; eight rows on, they are the same but for the rows' bytes
+  uint32_t q_off[KS / 2];
+#pragma unroll
+  for (int ks = 0; ks < KS; ks += 2) q_off[ks / 2] = half_at<HD>(lane & 7, 2 * ks + (lane >> 3));
+
+  // ---- half a row a thread: asked for, then written as fp16 after a power of two, as in QFrag
+  alignas(16) T raw[DPT];
+  float lse_raw = 0.f;
+  const int my = tid >> 1, d0 = (tid & 1) * DPT;
+  auto ask = [&](int row0) {
+    const int r = row0 + my;
+    const T* p = qs + (r < R ? (long)(r / G) * at.q_ld + (r % G) * HD + d0 : 0);
+    constexpr int VEC = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < DPT; i += VEC) {
+      if (vec) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < R) x = *reinterpret_cast<const uint4*>(p + i);
+        *reinterpret_cast<uint4*>(raw + i) = x;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+          raw[i + j] = from_f<T>(0.f);
+          if (r < R) raw[i + j] = p[i + j];
+        }
+      }
+    }
+    if (!(tid & 1) && r < R) lse_raw = at.lse[(long)(r0 + r / G) * (a.H * G) + h * G + r % G];
+  };
+  auto put = [&](int row0, int buf) {
+    const int r = row0 + my;
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < DPT; i++) top = fmaxf(top, fabsf(to_f<T>(raw[i])));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+    e = min(max(e, -100), 100);
+    const float up = kv8_pow2(e);
+    uint8_t* to = smem + buf * TERMS * TILE;
+#pragma unroll
+    for (int i = 0; i < DPT; i += 2) {
+      const float lo = to_f<T>(raw[i]) * up, hi = to_f<T>(raw[i + 1]) * up;
+      const uint32_t v = pack_f16(lo, hi);
+      // (half a row of dimensions is half of the places of each step: d0 moves t by two)
+      const int place = half_place<HD>(i) + (HD == 128 ? (tid & 1) * 64 : (tid & 1) * 4);
+      const uint32_t off = half_at<HD>(my, place >> 3) + (place & 7) * 2;
+      *reinterpret_cast<uint32_t*>(to + off) = v;
+      if (TERMS == 2) *reinterpret_cast<uint32_t*>(to + TILE + off) = pack_rest(lo, hi, v);
+    }
+    if (!(tid & 1)) {
+      const bool on = r < R && lse_raw != -INFINITY;  // else: no row, or one without weights
+      r_f[buf][my] = kv8_pow2(-e) * at.scale * 1.4426950408889634f;
+      r_ls[buf][my] = on ? lse_raw * 1.4426950408889634f : 0.f;
+      r_see[buf][my] = on ? min(len + r / G + 1, cap) : 0;
+    }
+  };
+
   // the grid covers the caller's bound on the lengths; a longer sequence takes its blocks further
-  for (long first = (long)(blockIdx.x * (blockDim.x >> 5) + w) * TW * TT; first < see_hi;
-       first += (long)gridDim.x * (blockDim.x >> 5) * TW * TT) {
-    const int base = (int)first;
-    uint32_t kw[2 * TW][2][KS];
-    int blk[2 * TW];
-    float ks[2 * TW];
+  for (long first = (long)blockIdx.x * AT; first < see_hi; first += (long)gridDim.x * AT) {
+    const int base = (int)first + w * 32;  // the warp's slots
+    // rows before this one see nothing of the block's slots
+    const int start = (int)(max(0L, first - len) * G / AR) * AR;
+    ask(start);
+    uint32_t ka[2][KS][4];
+    int blk[2];
+    float ks[2];
 #pragma unroll
-    for (int x = 0; x < 2 * TW; x++) blk[x] = base + x * 16 < see_hi ? kv8_block(a, s, (base + x * 16) >> a.lgP) : -1;
-#pragma unroll
-    for (int x = 0; x < 2 * TW; x++) {
+    for (int x = 0; x < 2; x++) {
+      const int j0 = base + x * 16;
+      blk[x] = j0 < see_hi ? kv8_block(a, s, j0 >> a.lgP) : -1;
       const size_t bh = (size_t)max(blk[x], 0) * a.H + h;
       ks[x] = blk[x] >= 0 ? a.ks[bh] : 0.f;
 #pragma unroll
       for (int half = 0; half < 2; half++) {
-        const int j = base + x * 16 + key_token(g, half);
+        const int j = j0 + g + 8 * half;
         const uint8_t* p = a.k + ((bh << a.lgP) + (j & (a.P - 1))) * HD;
         const bool on = blk[x] >= 0 && j < see_hi;
+        uint32_t kw[KS];
         if (HD == 32) {
           const uint2 c = on ? *reinterpret_cast<const uint2*>(p + t * 8) : make_uint2(0, 0);
-          kw[x][half][0] = c.x, kw[x][half][1] = c.y;
+          kw[0] = c.x, kw[1] = c.y;
         } else {
 #pragma unroll
           for (int i = 0; i < HD / 64; i++) {
             const uint4 c = on ? *reinterpret_cast<const uint4*>(p + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-            kw[x][half][(4 * i) % KS] = c.x, kw[x][half][(4 * i + 1) % KS] = c.y;
-            kw[x][half][(4 * i + 2) % KS] = c.z, kw[x][half][(4 * i + 3) % KS] = c.w;
+            kw[(4 * i) % KS] = c.x, kw[(4 * i + 1) % KS] = c.y, kw[(4 * i + 2) % KS] = c.z, kw[(4 * i + 3) % KS] = c.w;
           }
+        }
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          ka[x][k][half] = f16x2_e4m3(kw[k]);
+          ka[x][k][2 + half] = f16x2_e4m3(kw[k] >> 16);
         }
       }
     }
-    float sum[2 * TW][2];
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    int buf = 0;
+    __syncthreads();  // every warp is done with the tiles of the slots before
+    for (int row0 = start; row0 < R; row0 += AR, buf ^= 1) {
+      put(row0, buf);
+      __syncthreads();
+      if (row0 + AR < R) ask(row0 + AR);
+      const int last = min(R - 1, row0 + AR - 1);
+      if (base >= min(len + last / G + 1, cap)) continue;  // no row of these sees the warp's slots
+      const bool full = row0 + AR <= R && base + 32 <= min(len + row0 / G + 1, cap);
+      const uint32_t qb = (uint32_t)__cvta_generic_to_shared(smem) + buf * TERMS * TILE;
 #pragma unroll
-    for (int x = 0; x < 2 * TW; x++) sum[x][0] = sum[x][1] = 0.f;
-    for (int row0 = 0; row0 < R; row0 += ROWS) {
-      if (base >= len + min(R - 1, row0 + ROWS - 1) / G + 1) continue;  // no row of these sees the warp's slots
-      QFrag<T, HD, NT> q;
-      q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, row0, R, at.scale);
-      float ls[NT][2];
-      int see[NT][2];
+      for (int nt = 0; nt < AR / 8; nt++) {
+        float d[2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; nt++)
+        for (int x = 0; x < 2; x++) d[x][0] = d[x][1] = d[x][2] = d[x][3] = 0.f;
+#pragma unroll
+        for (int term = 0; term < TERMS; term++)
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t b[4];
+            ldsm4(b, qb + term * TILE + q_off[k / 2] + nt * 16 * HD);
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+              mma(d[x], ka[x][k][0], ka[x][k][1], ka[x][k][2], ka[x][k][3], b[0], b[1]);
+              mma(d[x], ka[x][k + 1][0], ka[x][k + 1][1], ka[x][k + 1][2], ka[x][k + 1][3], b[2], b[3]);
+            }
+          }
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          const int r = row0 + 8 * nt + 2 * t + e, i = min(r, R - 1) / G;
-          see[nt][e] = r < R ? min(len + i + 1, cap) : 0;  // rows past the last see nothing
-          const float x = r < R ? at.lse[(long)(r0 + i) * (a.H * G) + h * G + r % G] : 0.f;
-          if (x == -INFINITY) see[nt][e] = 0;  // a row without weights
-          ls[nt][e] = x * 1.4426950408889634f;
-        }
+          const int r = 8 * nt + 2 * t + e;
+          const float f = r_f[buf][r], ls = r_ls[buf][r];
+          const int see = r_see[buf][r];
 #pragma unroll
-      for (int x = 0; x < 2 * TW; x++) {
-        float d[NT][4];
-        q.qk(d, kw[x][0], kw[x][1]);
+          for (int x = 0; x < 2; x++) {
+            const float fk = f * ks[x];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int half = 0; half < 2; half++) {
-            const int j = base + x * 16 + key_token(g, half);
-#pragma unroll
-            for (int e = 0; e < 2; e++)
-              sum[x][half] += j < see[nt][e] ? sfu_exp2(d[nt][2 * half + e] * (q.f[nt][e] * ks[x]) - ls[nt][e]) : 0.f;
+            for (int half = 0; half < 2; half++) {
+              const float p = sfu_exp2(fmaf(d[x][2 * half + e], fk, -ls));
+              sum[x][half] += (full ? see > 0 : base + x * 16 + g + 8 * half < see) ? p : 0.f;
+            }
           }
+        }
       }
     }
 #pragma unroll
-    for (int x = 0; x < 2 * TW; x++)
+    for (int x = 0; x < 2; x++) {
 #pragma unroll
       for (int half = 0; half < 2; half++) {
-        float v = sum[x][half];
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        const int j = base + x * 16 + key_token(g, half);
-        // one of the four lanes that hold the sum adds it (atomically: two sequences may share a block)
-        if (t == half && j < see_hi && blk[x] >= 0)
-          atomicAdd(a.w + ((((size_t)blk[x] * a.H + h) << a.lgP) + (j & (a.P - 1))), v);
+        sum[x][half] += __shfl_xor_sync(0xffffffffu, sum[x][half], 1);
+        sum[x][half] += __shfl_xor_sync(0xffffffffu, sum[x][half], 2);
       }
+      // one of the four lanes that hold a sum adds it (atomically: two sequences may share a block)
+      const int j = base + x * 16 + g + 8 * (t & 1);
+      if (t < 2 && j < see_hi && blk[x] >= 0)
+        atomicAdd(a.w + ((((size_t)blk[x] * a.H + h) << a.lgP) + (j & (a.P - 1))), t ? sum[x][1] : sum[x][0]);
+    }
   }
 }
 
@@ -1205,27 +1298,30 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   return launch_attn_many<T, HD, TK, HD == 128 || sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
 }
 
-template <typename T, int HD, int NT>
-void launch_accumulate(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
-  constexpr int TW = HD == 128 ? 1 : 2;
-  const int per = 8 * TW * TT;
-  k_kv8_accumulate<T, HD, NT, TW><<<dim3((max_len + per - 1) / per, a.H, a.S), 256, 0, c.stream>>>(a, at);
+template <typename T, int HD>
+bool launch_accumulate_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  constexpr int TERMS = sizeof(T) == 4 ? 2 : 1, SMEM = 2 * TERMS * AR * HD * 2, MINB = HD == 128 ? 2 : sizeof(T) == 4 ? 3 : 4;
+  constexpr auto kernel = k_kv8_accumulate_many<T, HD, MINB>;
+  if (!allow_smem<kernel>(SMEM)) return false;
+  kernel<<<dim3((max_len + AT - 1) / AT, a.H, a.S), 128, SMEM, c.stream>>>(a, at);
+  return true;
 }
 template <typename T, int HD, int NT>
-void launch_accumulate_few(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+bool launch_accumulate_few(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   constexpr int MINB = HD == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 6 : 4;
   // a warp for every two tiles, but no more blocks than the GPU holds at once
   const long tiles = (max_len + TT - 1) / TT, most = (tiles + 7) / 8, pairs = (long)a.H * a.S;
   long split = (long)MINB * c.num_sms / pairs;
   split = split > most ? most : split < 1 ? 1 : split;
   k_kv8_accumulate_few<T, HD, NT, MINB><<<dim3((unsigned)split, a.H, a.S), 128, 0, c.stream>>>(a, at);
+  return true;
 }
 template <typename T, int HD>
-void launch_accumulate_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+bool launch_accumulate_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long rows = (long)a.max_new * at.G;
   if (rows <= 8) return launch_accumulate_few<T, HD, 1>(c, a, at, max_len);
   if (rows <= 16) return launch_accumulate_few<T, HD, 2>(c, a, at, max_len);
-  return launch_accumulate<T, HD, 2>(c, a, at, max_len);
+  return launch_accumulate_many<T, HD>(c, a, at, max_len);
 }
 
 }  // namespace
@@ -1244,7 +1340,7 @@ bool kv8_attention(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, cons
   return launch_attn_rows<float, 128>(c, a, at, max_len);
 }
 
-void kv8_accumulate(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, const void* q, long q_ld, float scale,
+bool kv8_accumulate(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, const void* q, long q_ld, float scale,
                     int max_len, const float* lse) {
   LaunchScope s(c, "kv8_accumulate");
   AttnArgs at{q, q_ld, scale, G, 0, nullptr, 0, const_cast<float*>(lse)};

@@ -121,9 +121,8 @@ extern "C" gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32
   const int G = n_head / a.H, cap = capacity(a);
   if ((int64_t)max_new * G > (1 << 30)) return GPT_ERR_UNSUPPORTED;
   return launch(cuda_stream, [&](Ctx& c) {
-    kv8_accumulate(c, a, cache->head_dim, G, rows_bf16 != 0, d_q, q_ld, scale,
-                   max_len == 0 || max_len > cap ? cap : max_len, d_lse);
-    return true;
+    return kv8_accumulate(c, a, cache->head_dim, G, rows_bf16 != 0, d_q, q_ld, scale,
+                          max_len == 0 || max_len > cap ? cap : max_len, d_lse);
   });
 }
 

@@ -110,7 +110,7 @@ void kv8_append(Ctx& c, const Kv8Args& a, int hd, bool bf16_rows, const void* k,
 // sequence goes by it).  False: the launch failed.
 bool kv8_attention(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, const void* q, long q_ld, float scale,
                    int max_len, void* o, long o_ld, float* lse);
-void kv8_accumulate(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, const void* q, long q_ld, float scale,
+bool kv8_accumulate(Ctx& c, const Kv8Args& a, int hd, int G, bool bf16_rows, const void* q, long q_ld, float scale,
                     int max_len, const float* lse);
 bool kv8_evict(Ctx& c, const Kv8Args& a, int hd, const int32_t* table_out, int max_blocks_out, int budget, int recent,
                int32_t* kept);

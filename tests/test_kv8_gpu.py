@@ -382,6 +382,43 @@ def test_accumulate(hd, P, H, G, lens, news, dtype):
     assert torch.equal(gpu2.weight, gpu.weight)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,P,H,G,lens,news,max_len", [
+    (64, 16, 1, 1, [150, 0, 31], [130, 70, 17], 0), (128, 32, 1, 2, [300, 5], [40, 9], 1), (32, 64, 2, 1, [200, 64], [65, 16], 0),
+    (64, 128, 1, 7, [50], [19], 1), (32, 16, 1, 3, [7], [64], 100)])
+def test_accumulate_many_rows(hd, P, H, G, lens, news, max_len, dtype):
+    """More rows than a decoding step has, over several tiles of rows and blocks of slots, the grid smaller than the
+    sequence (the bound on the lengths is a hint), a sequence with blocks outside the pool, and rows at an odd offset."""
+    gpu, ref, rng = make(21, [a + b for a, b in zip(lens, news)], H, hd, P)
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    table = ref.table.copy()
+    if len(lens) == 3:
+        table[1] = -7
+    ref.table = table
+    gpu.table = torch.from_numpy(table).cuda()
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), H * G, hd, dtype, gain=0.5)
+    out, lse, probs = check_attention(gpu, ref, q, q64, st, news, dtype, max_len=max_len)
+    before = gpu.weight.clone()
+    gpu.accumulate(q, lse, start=dev(st), max_new=max(news), max_len=max_len)
+    w0 = ref.weight.copy()
+    ref.accumulate(probs)
+    got = gpu.weight.cpu().numpy().astype(np.float64)
+    B = max(float(np.max(hd ** -0.5 * np.abs(ref.values(s, lens[s] + news[s], "k")[0][:, h // G])
+                         @ np.abs(q64[st[s]:st[s + 1], h]).T, initial=0.0))
+            for s in range(len(lens)) for h in range(H * G))
+    gain = ref.weight - w0
+    assert (np.abs(got - ref.weight) <= (2 * B + 4) * 2.0 ** -20 * gain + 2.0 ** -23 * ref.weight + 1e-30).all()
+    assert np.array_equal(got[gain == 0], before.double().cpu().numpy()[gain == 0])  # slots that no row sees
+    odd = torch.zeros(q.shape[0], q.shape[1] * hd + 1, dtype=q.dtype, device="cuda")
+    odd[:, 1:] = q.flatten(1)
+    first = gpu.weight.clone()
+    gpu.weight.copy_(before)
+    gpu.accumulate(odd[:, 1:].unflatten(1, q.shape[1:]), lse, start=dev(st), max_new=max(news), max_len=max_len)
+    assert torch.equal(gpu.weight, first)
+
+
 @pytest.mark.parametrize("H,hd,P,lens,budget,recent", [
     (2, 64, 16, [100, 30, 31, 64, 0, 1], 31, 7),
     (1, 128, 64, [1000], 257, 257),
