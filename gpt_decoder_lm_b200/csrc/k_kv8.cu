@@ -85,7 +85,9 @@ constexpr int AU = 4;  // units of 8 elements that a thread holds: 512 threads c
 // One thread block: the new tokens that fall into one cache block, of one
 // head, of K or of V (grid: touched block, 2 H, sequence).  HBM-bound: the
 // rows are read once, held as they came, and quantised after the block's
-// maximum is known.
+// maximum is known.  B200: 6800 bf16 tokens of 25 heads of 64 in 15.5 us, 65% of
+// the copy bandwidth (reads and writes do not overlap within a block); one token
+// for each of 12 sequences 2.7 us, a launch.
 template <typename T, int HD>
 __global__ void __launch_bounds__(512) k_kv8_append(Kv8Args a, const T* __restrict__ xk, long k_ld,
                                                     const T* __restrict__ xv, long v_ld, int vec) {
@@ -192,7 +194,9 @@ __device__ __forceinline__ uint32_t slot_key(const Kv8Args& a, int s, int h, int
 // of the others, the `budget - recent` heaviest (ties: the lowest slots).  The
 // threshold key is found digit by digit, from the top; the kept slots are then
 // written in order from counts of each warp's range.  A cluster of blocks takes
-// a head, each an equal part of its slots.
+// a head, each an equal part of its slots.  Bound by barriers (B200: 768 heads of
+// up to 1023 slots 13 us; 48 heads of up to 40000 slots, eight blocks each, 24 us,
+// before the cluster 49 us).
 template <int ET, bool SMEM>
 __global__ void __launch_bounds__(ET, ET == 256 ? 6 : 3) k_kv8_select(Kv8Args a, int budget, int recent, int32_t* __restrict__ kept) {
   constexpr int EW = ET / 32;
@@ -394,7 +398,8 @@ __device__ __forceinline__ uint4 chunk_scale(const uint4& v, int k) {
 // codes are read from their blocks, the destination's exponents are found anew
 // from their values, and the codes are written at them.  Bound by the chain of
 // loads (kept slot, block id, scale and codes): every thread follows it for its
-// own MU chunks of K and of V.
+// own MU chunks of K and of V.  B200: 393,600 tokens of 128 in 42 us (75% of the
+// copy bandwidth), 393,200 of 64 in blocks of 16 in 23 us (66%).
 template <int WPU, int MU>
 __global__ void __launch_bounds__(MT) k_kv8_move(Kv8Args a, int hd, const int32_t* __restrict__ table_out,
                                                  int max_blocks_out, int budget, const int32_t* __restrict__ kept) {
