@@ -278,8 +278,8 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
 // at the end in a fixed order.
 //
 // B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 67.5 us, 85%
-// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 20.5
-// us (8.6 us at the copy bandwidth): about 4 us pass before the first tile (start,
+// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 19.9
+// us (8.6 us at the copy bandwidth): about 3 us pass before the first tile (start,
 // length, table, codes), a warp's tile of 32 slots takes some 540 cycles of its
 // scheduler (64 conversions at 2, 16 MMA at 12.5, the rest softmax), and SMs with
 // longer sequences finish last.
@@ -296,11 +296,22 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   const int n_split = at.n_split, split = blockIdx.x % n_split, rt = blockIdx.x / n_split;
   const int h = blockIdx.y, s = blockIdx.z;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  // The length, the first tile's block ids (the first part's tiles start at 0 whatever the length) and the rows are
+  // asked for together, not one after the other.
+  const int32_t* ids = a.table + (size_t)s * a.max_blocks;
+  const int len_raw = a.len[s];
+  int pre0 = -1, pre1 = -1;
+  if (split == 0) {
+    if ((w * TT) >> a.lgP < a.max_blocks) pre0 = ids[(w * TT) >> a.lgP];
+    if ((w * TT + 16) >> a.lgP < a.max_blocks) pre1 = ids[(w * TT + 16) >> a.lgP];
+  }
   int r0;
-  const int n = kv8_rows(a, s, &r0), len = kv8_len(a, s), G = at.G;
+  const int n = kv8_rows(a, s, &r0), G = at.G;
   const int R = n * G, row0 = rt * ROWS;
   if (row0 >= R) return;  // the same for every block of the cluster
-  const int cap = a.max_blocks << a.lgP;
+  QFrag<T, HD, NT> q;
+  q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, row0, R, at.scale);
+  const int cap = a.max_blocks << a.lgP, len = min(max(len_raw, 0), cap);
   const int see_lo = min(len + row0 / G + 1, cap), see_hi = min(len + min(R - 1, row0 + ROWS - 1) / G + 1, cap);
 
   float o[MT][NT][4];
@@ -331,7 +342,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   auto look = [&](int tile) {
     b0 = b1 = -1;
     if (tile < t1) {
-      const int32_t* ids = a.table + (size_t)s * a.max_blocks;
       b0 = ids[(tile * TT) >> a.lgP];
       if (tile * TT + 16 < see_hi) b1 = ids[(tile * TT + 16) >> a.lgP];
     }
@@ -384,15 +394,18 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   };
 
   int next = t0 + w;
-  look(next);
+  if (split == 0) {
+    if (next < t1) b0 = pre0;
+    if (next < t1 && next * TT + 16 < see_hi) b1 = pre1;
+  } else {
+    look(next);
+  }
 #pragma unroll
   for (int i = 0; i < NS - 1; i++) {
     request(next, i);
     next += NW;
     look(next);
   }
-  QFrag<T, HD, NT> q;
-  q.load(reinterpret_cast<const T*>(at.q) + (long)r0 * at.q_ld + h * G * HD, at.q_ld, G, row0, R, at.scale);
   int slot = 0;
   for (int tile = t0 + w; tile < t1; tile += NW) {
     cp_wait<NS - 2>();
