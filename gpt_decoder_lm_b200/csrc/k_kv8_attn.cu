@@ -277,8 +277,8 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
 // warps, then the cluster's blocks through distributed shared memory, are joined
 // at the end in a fixed order.
 //
-// B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 67.5 us, 85%
-// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 19.9
+// B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 65.3 us, 87%
+// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 18.9
 // us (8.6 us at the copy bandwidth): about 3 us pass before the first tile (start,
 // length, table, codes), a warp's tile of 32 slots takes some 540 cycles of its
 // scheduler (64 conversions at 2, 16 MMA at 12.5, the rest softmax), and SMs with
@@ -472,24 +472,20 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         const float big[2] = {fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])};
-        float x = fmaxf(big[0], big[1]);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        float y = x + v0;
-        if (v0 != v1) {
-          y = fmaxf(big[0] + v0, big[1] + v1);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-        }
-        top[nt][e] = x;
-        topv[nt][e] = y;
-        grow |= x > m[nt][e] + LAZY || y > mv[nt][e] + LAZY;
+        top[nt][e] = fmaxf(big[0], big[1]);
+        topv[nt][e] = fmaxf(big[0] + v0, big[1] + v1);
+        grow |= top[nt][e] > m[nt][e] + LAZY || topv[nt][e] > mv[nt][e] + LAZY;
       }
-    if (__any_sync(0xffffffffu, grow)) {
+    if (__any_sync(0xffffffffu, grow)) {  // the lanes' maxima are brought together only where one of them says so
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], d));
+            topv[nt][e] = fmaxf(topv[nt][e], __shfl_xor_sync(0xffffffffu, topv[nt][e], d));
+          }
           const float m1 = fmaxf(m[nt][e], top[nt][e]), mv1 = fmaxf(mv[nt][e], topv[nt][e]);
           const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[nt][e] - m1);
           const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[nt][e] - mv1);
@@ -882,16 +878,16 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
         top[half] = fmaxf(top[half], x);
         topv[half] = fmaxf(topv[half], x + vl[gr]);
       }
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], d));
-        topv[half] = fmaxf(topv[half], __shfl_xor_sync(0xffffffffu, topv[half], d));
-      }
       grow |= top[half] > m[half] + LAZY || topv[half] > mv[half] + LAZY;
     }
-    if (__any_sync(0xffffffffu, grow)) {
+    if (__any_sync(0xffffffffu, grow)) {  // the lanes' maxima are brought together only where one of them says so
 #pragma unroll
       for (int half = 0; half < 2; half++) {
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], d));
+          topv[half] = fmaxf(topv[half], __shfl_xor_sync(0xffffffffu, topv[half], d));
+        }
         const float m1 = fmaxf(m[half], top[half]), mv1 = fmaxf(mv[half], topv[half]);
         const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[half] - m1);
         const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[half] - mv1);
