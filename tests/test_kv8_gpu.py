@@ -471,6 +471,43 @@ def test_evict_ties_keep_the_lowest_slots_and_long_sequences():
         assert kept[0, 0].tolist() == sorted(h | set(rest)) + list(range(n - recent, n))
 
 
+@pytest.mark.parametrize("P,most", [(16, 700), (128, 1024), (32, 1025), (64, 2048), (16, 2064)])
+@pytest.mark.parametrize("kind", ["spread", "few values", "one value", "two values far apart", "negative and infinite"])
+def test_evict_selection(P, most, kind):
+    """The kept slots at the capacities where the selection changes its form, for weights that separate early, late or
+    not at all, and budgets at both ends."""
+    lens = [most, most - 1, most // 2, 3]
+    gpu, ref, rng = make(60, lens, 2, 32, P)
+    out_cap = -(-most // P)
+    n = ref.k.shape[0]
+    shape = ref.weight.shape
+    w = {"spread": rng.random(shape) ** 4 * 8, "few values": rng.integers(0, 4, shape) * 0.25, "one value": np.full(shape, 0.5),
+         "two values far apart": np.where(rng.random(shape) < 0.5, 1e-30, 1e30),
+         "negative and infinite": np.where(rng.random(shape) < 0.1, np.inf, rng.standard_normal(shape))}[kind].astype(np.float32)
+    grown = torch.zeros(n + 4 * out_cap, *gpu.k.shape[1:], dtype=torch.uint8, device="cuda")
+    grown[:n] = gpu.k
+    weight = torch.zeros(n + 4 * out_cap, *shape[1:], device="cuda")
+    weight[:n] = torch.from_numpy(w).cuda()
+    scale = torch.ones(n + 4 * out_cap, 2, device="cuda")
+    c = gb.KV8Cache(grown, grown.clone(), scale, scale.clone(), gpu.table, gpu.length, weight, gpu.flags)
+    to = torch.arange(n, n + 4 * out_cap, dtype=torch.int32, device="cuda").reshape(4, out_cap)
+    for budget, recent in ((1, 0), (most // 3, 5), (most - 1, 1), (most // 2, most // 2), (most, 0)):
+        kept = torch.full((4, 2, budget), -9, dtype=torch.int32, device="cuda")
+        c.evict(to, budget, recent, kept)
+        got = kept.cpu().numpy()
+        for s, length in enumerate(lens):
+            for h in range(2):
+                ws = np.concatenate([w[b, h] for b in ref.table[s]])[:length].astype(np.float64)
+                if length <= budget:
+                    want = np.concatenate([np.arange(length), np.full(budget - length, -1)])
+                else:
+                    m = length - recent
+                    heavy = np.lexsort((np.arange(m), -ws[:m]))[:budget - recent]
+                    want = np.concatenate([np.sort(heavy), np.arange(m, length)])
+                assert np.array_equal(got[s, h], want), (budget, recent, s, h)
+    assert int(c.flags) == 0
+
+
 def test_a_run_of_steps_with_eviction():
     """Append, attention, accumulation, eviction and advance over many steps, as decoding uses them."""
     rng = np.random.default_rng(40)
