@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 
 #include "kv8.cuh"
+#include "sm100.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -966,6 +967,393 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   join_blocks<T, HD, MR, OP, MW * 32>(stats, part, n_split, split, min(MR, R - row0), at, r0, row0, h, a.H * G);
 }
 
+// ---------------------------------------------------------------- many rows of bf16: tcgen05
+//
+// 128 rows of one key / value head and sequence over one of the cluster's equal
+// parts of the slots, 64 slots a tile.  Two warps turn codes into fp16 tiles
+// (128-byte swizzle, as a TMA load would leave them) through a ring of stages;
+// one thread issues S = Q K^T into one of two TMEM buffers and, a tile later,
+// O += P V with P read from TMEM; four warps, a row a thread, do the softmax:
+// scores are scaled by the row's and the group's factors, P goes back to TMEM as
+// fp16 over its scores, and O is rescaled in TMEM only where a running maximum
+// has to grow.  Statistics and joins are those of k_kv8_attn.
+constexpr int CR = 128, CT = 64;             // rows of a block, slots of a tile
+constexpr int C_SOFT = 4, C_MAKE = 2;        // softmax and converting warps; one more issues
+constexpr int C_THREADS = (C_SOFT + 1 + C_MAKE) * 32;
+
+template <int HD>
+struct TcShape {
+  static constexpr int NB = HD == 128 ? 2 : 1, WD = HD < 64 ? HD : 64;  // blocks of 64 dimensions, dimensions a block
+  static constexpr int NS = HD == 128 ? 2 : 3;                          // stages
+  static constexpr int QB = CR * 128, TB = CT * 128;                    // bytes of a block's Q, and of K or V
+  static constexpr int KV = NB * QB, STAGE = 2 * NB * TB;               // the first stage; K blocks, then V blocks
+  static constexpr int END = KV + NS * STAGE, PITCH = HD + 4;           // (later: outputs [CR][PITCH])
+  static_assert(CR * PITCH * 4 <= END, "the outputs take the tiles' place");
+};
+struct TcShared {
+  RowStats<CR> stats;
+  uint64_t q_full, kv_full[3], kv_empty[3], s_full[2], p_full[2], pv_done[2];
+  float ks[3][4], vl[3][4];  // a stage's groups: K scale, log2 of the V scale (-infinity: no block)
+  int nan[3][C_MAKE];        // a NaN has been taken out of the stage's V
+  uint32_t tmem, no_flags;
+  int abort;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
+  using S = TcShape<HD>;
+  using namespace sm100;
+  constexpr int CPR = HD / 16, CPT = CT * CPR / (C_MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
+  extern __shared__ uint8_t raw_smem[];
+  // swizzled tiles need 1024-byte alignment
+  uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  TcShared& sh = *reinterpret_cast<TcShared*>(smem + S::END);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_split = at.n_split, split = blockIdx.x % n_split, rt = blockIdx.x / n_split;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int32_t* ids = a.table + (size_t)s * a.max_blocks;
+  const int len_raw = a.len[s];
+  int r0;
+  const int n = kv8_rows(a, s, &r0), G = at.G;
+  const int R = n * G, row0 = rt * CR;
+  if (row0 >= R) return;  // the same for every block of the cluster
+  const int cap = a.max_blocks << a.lgP, len = min(max(len_raw, 0), cap);
+  const int see_lo = min(len + row0 / G + 1, cap), see_hi = min(len + min(R - 1, row0 + CR - 1) / G + 1, cap);
+  const int tiles = (see_hi + CT - 1) / CT, per = (tiles + n_split - 1) / n_split;
+  const int t0 = min(tiles, split * per), nt = min(tiles, t0 + per) - t0;
+  uint32_t* gflags = a.flags ? a.flags : &sh.no_flags;
+  volatile int* abort_flag = &sh.abort;
+  const uint32_t q_full = smem_u32(&sh.q_full), kv_full0 = smem_u32(sh.kv_full), kv_empty0 = smem_u32(sh.kv_empty);
+  const uint32_t s_full0 = smem_u32(sh.s_full), p_full0 = smem_u32(sh.p_full), pv_done0 = smem_u32(sh.pv_done);
+
+  if (tid == 0) {
+    mbar_init(q_full, C_SOFT);
+    for (int i = 0; i < 3; i++) {
+      mbar_init(kv_full0 + 8 * i, C_MAKE);
+      mbar_init(kv_empty0 + 8 * i, 1);
+    }
+    for (int u = 0; u < 2; u++) {
+      mbar_init(s_full0 + 8 * u, 1);
+      mbar_init(p_full0 + 8 * u, C_SOFT);
+      mbar_init(pv_done0 + 8 * u, 1);
+    }
+    sh.abort = 0;
+    sh.no_flags = 0;
+    fence_barrier_init();
+  }
+  if (warp == C_SOFT) {
+    tmem_alloc(smem_u32(&sh.tmem), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp > C_SOFT) {
+    // ================= codes to fp16 tiles
+    const int me = tid - (C_SOFT + 1) * 32, w = warp - C_SOFT - 1;
+    const int trow = me / CPR, part = me % CPR;
+    constexpr int STEP = C_MAKE * 32 / CPR;  // rows between a thread's chunks
+    int blk[CPT], gblk = -1;
+    uint4 ck[CPT], cv[CPT];
+    float gks = 0.f, gvs = 0.f;  // 0: no block
+    auto look = [&](int j) {
+#pragma unroll
+      for (int u = 0; u < CPT; u++) {
+        const int slot = (t0 + j) * CT + trow + u * STEP;
+        blk[u] = -1;
+        if (j < nt && slot < see_hi) blk[u] = ids[slot >> a.lgP];  // first touched when the tile is fetched
+      }
+      gblk = -1;
+      if (me < 4 && j < nt && (t0 + j) * CT + me * 16 < see_hi) gblk = ids[((t0 + j) * CT + me * 16) >> a.lgP];
+    };
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int u = 0; u < CPT; u++) {
+        ck[u] = cv[u] = make_uint4(0, 0, 0, 0);
+        if ((unsigned)blk[u] < (unsigned)a.n_blocks) {
+          const int slot = (t0 + j) * CT + trow + u * STEP;
+          const size_t src = ((((size_t)blk[u] * a.H + h) << a.lgP) + (slot & (a.P - 1))) * HD + part * 16;
+          ck[u] = *reinterpret_cast<const uint4*>(a.k + src);
+          cv[u] = *reinterpret_cast<const uint4*>(a.v + src);
+        }
+      }
+      if (me < 4 && j < nt) {
+        const bool on = (unsigned)gblk < (unsigned)a.n_blocks;
+        if (!on && (t0 + j) * CT + me * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
+        const size_t bh = (size_t)(on ? gblk : 0) * a.H + h;
+        gks = gvs = 0.f;
+        if (on) gks = a.ks[bh], gvs = a.vs[bh];
+      }
+    };
+    look(0);
+    fetch(0);
+    look(1);
+    for (int j = 0; j < nt; j++) {
+      const int st = j % S::NS;
+      if (!mbar_wait(kv_empty0 + 8 * st, ((j / S::NS) & 1) ^ 1, abort_flag, gflags)) break;
+      uint8_t* tk = smem + S::KV + st * S::STAGE;
+      uint8_t* tv = tk + S::NB * S::TB;
+      const int tile = t0 + j;
+      // a NaN that some of the rows do not see must not reach them as 0 * NaN: in a tile that not every row sees whole
+      // it is taken out of V, and put into the rows that see it at the end
+      const bool partial = tile * CT + CT > see_lo && see_lo != see_hi;
+      bool nan = false;
+#pragma unroll
+      for (int u = 0; u < CPT; u++) {
+        const int row = trow + u * STEP;
+        uint32_t x[4] = {ck[u].x, ck[u].y, ck[u].z, ck[u].w}, y[4] = {cv[u].x, cv[u].y, cv[u].z, cv[u].w};
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const uint32_t bad = (((y[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+            nan |= bad != 0;
+            y[i] &= ~(bad * 0xffu);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const uint32_t off = (part / 4) * S::TB + half_at<64>(row, part % 4 * 2 + i);
+          *reinterpret_cast<uint4*>(tk + off) =
+              make_uint4(f16x2_e4m3(x[2 * i]), f16x2_e4m3(x[2 * i] >> 16), f16x2_e4m3(x[2 * i + 1]), f16x2_e4m3(x[2 * i + 1] >> 16));
+          *reinterpret_cast<uint4*>(tv + off) =
+              make_uint4(f16x2_e4m3(y[2 * i]), f16x2_e4m3(y[2 * i] >> 16), f16x2_e4m3(y[2 * i + 1]), f16x2_e4m3(y[2 * i + 1] >> 16));
+        }
+      }
+      if (me < 4) {
+        sh.ks[st][me] = gks;
+        sh.vl[st][me] = gvs > 0.f ? (float)((int)(__float_as_uint(gvs) >> 23) - 127) : -INFINITY;
+      }
+      nan = __any_sync(0xffffffffu, nan);
+      if (lane == 0) sh.nan[st][w] = nan;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_full0 + 8 * st);
+      fetch(j + 1);
+      look(j + 2);
+    }
+  } else if (warp == C_SOFT) {
+    // ================= the products
+    if (lane == 0 && nt > 0) {
+      // D fp32, A and B fp16; 128 rows; S: 64 slots, O: a block's dimensions, V with the dimensions outermost
+      constexpr uint32_t id_s = (1u << 4) | ((CT >> 3) << 17) | ((CR >> 4) << 24);
+      constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((S::WD >> 3) << 17) | ((CR >> 4) << 24);
+      bool ok = mbar_wait(q_full, 0, abort_flag, gflags);
+      auto issue_pv = [&](int i) -> bool {
+        const int u = i & 1;
+        if (!mbar_wait(p_full0 + 8 * u, (i >> 1) & 1, abort_flag, gflags)) return false;
+        tc_fence_after();
+        const uint32_t v = sb + S::KV + (i % S::NS) * S::STAGE + S::NB * S::TB;
+#pragma unroll
+        for (int nb = 0; nb < S::NB; nb++)
+#pragma unroll
+          for (int kk = 0; kk < CT / 16; kk++)
+            mma_bf16_ts(tmem + 128 + 64 * nb, tmem + 64 * u + 8 * kk, desc_sw128(v + nb * S::TB + kk * 2048, S::TB, 1024), id_o,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(pv_done0 + 8 * u);
+        mma_commit(kv_empty0 + 8 * (i % S::NS));
+        return true;
+      };
+      for (int j = 0; j < nt && ok; j++) {
+        const int st = j % S::NS;
+        if (!(ok = mbar_wait(kv_full0 + 8 * st, (j / S::NS) & 1, abort_flag, gflags))) break;
+        tc_fence_after();
+        // S[j & 1] is free: its previous tile's P (j - 2) was waited for below
+        const uint32_t k = sb + S::KV + st * S::STAGE;
+#pragma unroll
+        for (int nb = 0; nb < S::NB; nb++)
+#pragma unroll
+          for (int kk = 0; kk < S::WD / 16; kk++)
+            mma_bf16_ss(tmem + 64 * (j & 1), desc_sw128(sb + nb * S::QB + kk * 32, 16, 1024),
+                        desc_sw128(k + nb * S::TB + kk * 32, 16, 1024), id_s, nb > 0 || kk > 0);
+        mma_commit(s_full0 + 8 * (j & 1));
+        if (j >= 1 && !(ok = issue_pv(j - 1))) break;
+      }
+      if (ok) issue_pv(nt - 1);
+    }
+    __syncwarp();
+  } else {
+    // ================= a row a thread
+    const int r = tid, rr = row0 + r;
+    const bool on = rr < R;
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    float qf = 0.f;
+    if (nt > 0) {
+      // fp16 after a power of two, as in QFrag
+      const bf16* p = reinterpret_cast<const bf16*>(at.q) + (on ? (long)(r0 + rr / G) * at.q_ld + (long)(h * G + rr % G) * HD : 0);
+      const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+      uint4 x[HD / 8];
+#pragma unroll
+      for (int i = 0; i < HD / 8; i++) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (on) {
+          if (vec) {
+            x[i] = reinterpret_cast<const uint4*>(p)[i];
+          } else {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(p) + 8 * i;
+            x[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                              e[6] | (uint32_t)e[7] << 16);
+          }
+        }
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < HD / 8; i++) {
+        const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                    __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        top = max(top, max(m << 16, m & 0xffff0000u));
+      }
+      int e = top != 0 && top < 0x7f800000u ? 14 - ((int)(top >> 23) - 127) : 0;
+      e = min(max(e, -100), 100);
+      const float up = kv8_pow2(e);
+      qf = kv8_pow2(-e) * at.scale * 1.4426950408889634f;
+#pragma unroll
+      for (int i = 0; i < HD / 8; i++) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[j] = pack_f16(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+        *reinterpret_cast<uint4*>(smem + (i / 8) * S::QB + half_at<64>(r, i % 8)) = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const int see = min(len + min(rr, R - 1) / G + 1, cap);
+    float m = -INFINITY, mv = -INFINITY, l = 0.f;
+    uint32_t nan_dims[HD / 32];
+#pragma unroll
+    for (int i = 0; i < HD / 32; i++) nan_dims[i] = 0;
+    bool ok = true;
+    for (int j = 0; j < nt; j++) {
+      const int u = j & 1, st = j % S::NS, base = (t0 + j) * CT;
+      if (!(ok = mbar_wait(kv_full0 + 8 * st, (j / S::NS) & 1, abort_flag, gflags))) break;  // the stage's scales
+      if (!(ok = mbar_wait(s_full0 + 8 * u, (j >> 1) & 1, abort_flag, gflags))) break;
+      tc_fence_after();
+      uint32_t v[2][32];
+      tmem_ld_32x32b_x32(trow + 64 * u, v[0]);
+      tmem_ld_32x32b_x32(trow + 64 * u + 32, v[1]);
+      float vl[4], gm[4];
+      bool all = base + CT <= see;
+      tmem_ld_wait();
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const float f = qf * sh.ks[st][g];
+        vl[g] = sh.vl[st][g];
+        all &= vl[g] != -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          uint32_t& x = v[g / 2][g % 2 * 16 + i];
+          x = __float_as_uint(__uint_as_float(x) * f);
+        }
+      }
+      if (!all) {
+#pragma unroll
+        for (int i = 0; i < CT; i++)
+          if (base + i >= see || vl[i / 16] == -INFINITY) v[i / 32][i % 32] = 0xff800000u;
+      }
+      float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          x0 = fmaxf(x0, __uint_as_float(v[g / 2][g % 2 * 16 + i]));
+          x1 = fmaxf(x1, __uint_as_float(v[g / 2][g % 2 * 16 + i + 1]));
+        }
+        gm[g] = fmaxf(x0, x1);
+        top = fmaxf(top, gm[g]);
+        topv = fmaxf(topv, gm[g] + vl[g]);
+      }
+      const bool need = top > m + LAZY || topv > mv + LAZY;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m1 = need ? fmaxf(m, top) : m, mv1 = need ? fmaxf(mv, topv) : mv;
+        const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m - m1), fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv - mv1);
+        m = m1, mv = mv1;
+        l *= fl;
+        if (j > 0) {
+          // O holds the products of the tiles before.  S of this tile was issued after P V of tile j - 2, so that of
+          // tile j - 1 is the only one that may be in flight.
+          if (!(ok = mbar_wait(pv_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag, gflags))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(trow + 128 + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+            tmem_st_32x32b_x16(trow + 128 + c, o);
+          }
+        }
+      }
+      const float mm = m == -INFINITY ? 0.f : m, dv = mm - (mv == -INFINITY ? 0.f : mv);
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int g = 0; g < 2; g++) {
+          const float c = sfu_exp2(vl[2 * half + g] + dv);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float e0 = sfu_exp2(__uint_as_float(v[half][16 * g + i]) - mm);
+            const float e1 = sfu_exp2(__uint_as_float(v[half][16 * g + i + 1]) - mm);
+            l += e0 + e1;
+            pk[8 * g + i / 2] = pack_f16(e0 * c, e1 * c);
+          }
+        }
+        // over the scores, which have been read: the A operand of P V
+        tmem_st_32x32b_x16(trow + 64 * u + 16 * half, pk);
+      }
+      tmem_st_wait();
+      if (sh.nan[st][0] | sh.nan[st][1]) {
+        for (int i = 0; i < CT && base + i < see; i++) {
+          const int b = ids[(base + i) >> a.lgP];
+          if ((unsigned)b >= (unsigned)a.n_blocks) continue;
+          const uint8_t* c = a.v + ((((size_t)b * a.H + h) << a.lgP) + ((base + i) & (a.P - 1))) * HD;
+#pragma unroll
+          for (int d = 0; d < HD; d++)
+            if ((c[d] & 0x7f) == 0x7f) nan_dims[d / 32] |= 1u << d % 32;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full0 + 8 * u);
+    }
+    // the last two products may both be in flight
+    if (ok && nt > 1) ok = mbar_wait(pv_done0 + 8 * (nt & 1), ((nt - 2) >> 1) & 1, abort_flag, gflags);
+    if (ok && nt > 0) ok = mbar_wait(pv_done0 + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, abort_flag, gflags);
+    tc_fence_after();
+    __syncwarp();
+    float* part = reinterpret_cast<float*>(smem) + r * S::PITCH;
+#pragma unroll
+    for (int c = 0; c < HD; c += 16) {
+      uint32_t o[16];
+#pragma unroll
+      for (int i = 0; i < 16; i++) o[i] = 0;
+      if (nt > 0) {  // (the same for all threads)
+        tmem_ld_32x32b_x16(trow + 128 + c, o);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if (nan_dims[(c + i) / 32] >> (c + i) % 32 & 1u) o[i] = 0x7fc00000u;
+      // every row's products are done (each thread has waited for the last), so that the tiles' place is free
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+    sh.stats.m[r] = m, sh.stats.mv[r] = mv, sh.stats.l[r] = l;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C_SOFT) tmem_dealloc(tmem, 256);
+  join_blocks<bf16, HD, CR, S::PITCH, C_THREADS>(sh.stats, reinterpret_cast<float*>(smem), n_split, split, min(CR, R - row0), at,
+                                                 r0, row0, h, a.H * G);
+}
+
 // ---------------------------------------------------------------- accumulation of the weights
 
 // weight[slot] += sum over the rows of exp(score - lse): the QK product again,
@@ -1309,6 +1697,13 @@ bool launch_attn_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   return launch_split<k_kv8_attn_many<T, HD, TK, MINB>>(c, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
 }
 
+template <int HD>
+bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
+  const long row_tiles = ((long)a.max_new * at.G + CR - 1) / CR;
+  const int split = split_of(c, (long)a.S * a.H * row_tiles, 2, (max_len + CT - 1) / CT, 2);
+  return launch_split<k_kv8_attn_tc<HD>>(c, a, at, split, row_tiles, C_THREADS, 1024 + TcShape<HD>::END + sizeof(TcShared));
+}
+
 template <typename T, int HD>
 bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long rows = (long)a.max_new * at.G;
@@ -1317,6 +1712,7 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   constexpr int NS = HD == 32 ? 4 : 2;
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
   if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
+  if constexpr (sizeof(T) == 2) return launch_attn_tc<HD>(c, a, at, max_len);
   constexpr int TK = HD == 128 && sizeof(T) == 4 ? 32 : 64;
   return launch_attn_many<T, HD, TK, HD == 128 || sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
 }
