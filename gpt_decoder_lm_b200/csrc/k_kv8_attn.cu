@@ -977,6 +977,14 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // scores are scaled by the row's and the group's factors, P goes back to TMEM as
 // fp16 over its scores, and O is rescaled in TMEM only where a running maximum
 // has to grow.  Statistics and joins are those of k_kv8_attn.
+//
+// B200: 2 sequences of 900 to 1000 new rows over 3000 to 4000 slots, 16 heads of
+// 64: 100 us, 310 TFLOP/s of the visible products (the warp MMA's blocks of 64
+// rows: 203 us).  Two resident blocks keep the SFU and the schedulers of the
+// softmax warps busy: a tile is 8192 exponentials at 16 a cycle and SM, and about
+// five other instructions each.  63 to 200 new rows over up to 1501 slots, 4
+// sequences of 25 heads: 28 us (33 us), two fifths of it before the first tile
+// and in the join.
 constexpr int CR = 128, CT = 64;             // rows of a block, slots of a tile
 constexpr int C_SOFT = 4, C_MAKE = 2;        // softmax and converting warps; one more issues
 constexpr int C_THREADS = (C_SOFT + 1 + C_MAKE) * 32;
@@ -1003,7 +1011,7 @@ template <int HD>
 __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
   using S = TcShape<HD>;
   using namespace sm100;
-  constexpr int CPR = HD / 16, CPT = CT * CPR / (C_MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
+  constexpr int CPR = HD / 16, CPT = (CT * CPR + C_MAKE * 32 - 1) / (C_MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
   extern __shared__ uint8_t raw_smem[];
   // swizzled tiles need 1024-byte alignment
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
@@ -1056,44 +1064,42 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
     const int me = tid - (C_SOFT + 1) * 32, w = warp - C_SOFT - 1;
     const int trow = me / CPR, part = me % CPR;
     constexpr int STEP = C_MAKE * 32 / CPR;  // rows between a thread's chunks
+    // the next tile's codes in flight, and the block ids of the tile behind it
     int blk[CPT], gblk = -1;
     uint4 ck[CPT], cv[CPT];
     float gks = 0.f, gvs = 0.f;  // 0: no block
     auto look = [&](int j) {
 #pragma unroll
       for (int u = 0; u < CPT; u++) {
-        const int slot = (t0 + j) * CT + trow + u * STEP;
+        const int row = trow + u * STEP, slot = (t0 + j) * CT + row;
         blk[u] = -1;
-        if (j < nt && slot < see_hi) blk[u] = ids[slot >> a.lgP];  // first touched when the tile is fetched
+        if (j < nt && row < CT && slot < see_hi) blk[u] = ids[slot >> a.lgP];  // first touched when the tile is fetched
       }
       gblk = -1;
       if (me < 4 && j < nt && (t0 + j) * CT + me * 16 < see_hi) gblk = ids[((t0 + j) * CT + me * 16) >> a.lgP];
     };
-    auto fetch = [&](int j) {
+    auto fetch = [&](int j, uint4 (&k)[CPT], uint4 (&v)[CPT], float& ks, float& vs) {
 #pragma unroll
       for (int u = 0; u < CPT; u++) {
-        ck[u] = cv[u] = make_uint4(0, 0, 0, 0);
+        k[u] = v[u] = make_uint4(0, 0, 0, 0);
         if ((unsigned)blk[u] < (unsigned)a.n_blocks) {
           const int slot = (t0 + j) * CT + trow + u * STEP;
           const size_t src = ((((size_t)blk[u] * a.H + h) << a.lgP) + (slot & (a.P - 1))) * HD + part * 16;
-          ck[u] = *reinterpret_cast<const uint4*>(a.k + src);
-          cv[u] = *reinterpret_cast<const uint4*>(a.v + src);
+          k[u] = *reinterpret_cast<const uint4*>(a.k + src);
+          v[u] = *reinterpret_cast<const uint4*>(a.v + src);
         }
       }
       if (me < 4 && j < nt) {
         const bool on = (unsigned)gblk < (unsigned)a.n_blocks;
         if (!on && (t0 + j) * CT + me * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
         const size_t bh = (size_t)(on ? gblk : 0) * a.H + h;
-        gks = gvs = 0.f;
-        if (on) gks = a.ks[bh], gvs = a.vs[bh];
+        ks = vs = 0.f;
+        if (on) ks = a.ks[bh], vs = a.vs[bh];
       }
     };
-    look(0);
-    fetch(0);
-    look(1);
-    for (int j = 0; j < nt; j++) {
+    auto make = [&](int j, const uint4 (&ckj)[CPT], const uint4 (&cvj)[CPT], float ks, float vs) -> bool {
       const int st = j % S::NS;
-      if (!mbar_wait(kv_empty0 + 8 * st, ((j / S::NS) & 1) ^ 1, abort_flag, gflags)) break;
+      if (!mbar_wait(kv_empty0 + 8 * st, ((j / S::NS) & 1) ^ 1, abort_flag, gflags)) return false;
       uint8_t* tk = smem + S::KV + st * S::STAGE;
       uint8_t* tv = tk + S::NB * S::TB;
       const int tile = t0 + j;
@@ -1104,7 +1110,8 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
 #pragma unroll
       for (int u = 0; u < CPT; u++) {
         const int row = trow + u * STEP;
-        uint32_t x[4] = {ck[u].x, ck[u].y, ck[u].z, ck[u].w}, y[4] = {cv[u].x, cv[u].y, cv[u].z, cv[u].w};
+        if (row >= CT) break;
+        uint32_t x[4] = {ckj[u].x, ckj[u].y, ckj[u].z, ckj[u].w}, y[4] = {cvj[u].x, cvj[u].y, cvj[u].z, cvj[u].w};
         if (partial) {
 #pragma unroll
           for (int i = 0; i < 4; i++) {
@@ -1123,15 +1130,22 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
         }
       }
       if (me < 4) {
-        sh.ks[st][me] = gks;
-        sh.vl[st][me] = gvs > 0.f ? (float)((int)(__float_as_uint(gvs) >> 23) - 127) : -INFINITY;
+        sh.ks[st][me] = ks;
+        sh.vl[st][me] = vs > 0.f ? (float)((int)(__float_as_uint(vs) >> 23) - 127) : -INFINITY;
       }
       nan = __any_sync(0xffffffffu, nan);
       if (lane == 0) sh.nan[st][w] = nan;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(kv_full0 + 8 * st);
-      fetch(j + 1);
+      return true;
+    };
+    look(0);
+    fetch(0, ck, cv, gks, gvs);
+    look(1);
+    for (int j = 0; j < nt; j++) {
+      if (!make(j, ck, cv, gks, gvs)) break;
+      fetch(j + 1, ck, cv, gks, gvs);
       look(j + 2);
     }
   } else if (warp == C_SOFT) {
@@ -1207,8 +1221,9 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
       }
       int e = top != 0 && top < 0x7f800000u ? 14 - ((int)(top >> 23) - 127) : 0;
       e = min(max(e, -100), 100);
-      const float up = kv8_pow2(e);
-      qf = kv8_pow2(-e) * at.scale * 1.4426950408889634f;
+      // a factor of the scores that is positive: the scale's sign goes with the row
+      const float up = copysignf(kv8_pow2(e), at.scale);
+      qf = fmaxf(kv8_pow2(-e) * fabsf(at.scale) * 1.4426950408889634f, 1e-36f);
 #pragma unroll
       for (int i = 0; i < HD / 8; i++) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -1235,20 +1250,15 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
       uint32_t v[2][32];
       tmem_ld_32x32b_x32(trow + 64 * u, v[0]);
       tmem_ld_32x32b_x32(trow + 64 * u + 32, v[1]);
-      float vl[4], gm[4];
+      float vl[4], f[4];
       bool all = base + CT <= see;
-      tmem_ld_wait();
 #pragma unroll
       for (int g = 0; g < 4; g++) {
-        const float f = qf * sh.ks[st][g];
         vl[g] = sh.vl[st][g];
+        f[g] = vl[g] == -INFINITY ? 1.f : qf * sh.ks[st][g];
         all &= vl[g] != -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          uint32_t& x = v[g / 2][g % 2 * 16 + i];
-          x = __float_as_uint(__uint_as_float(x) * f);
-        }
       }
+      tmem_ld_wait();
       if (!all) {
 #pragma unroll
         for (int i = 0; i < CT; i++)
@@ -1263,9 +1273,9 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
           x0 = fmaxf(x0, __uint_as_float(v[g / 2][g % 2 * 16 + i]));
           x1 = fmaxf(x1, __uint_as_float(v[g / 2][g % 2 * 16 + i + 1]));
         }
-        gm[g] = fmaxf(x0, x1);
-        top = fmaxf(top, gm[g]);
-        topv = fmaxf(topv, gm[g] + vl[g]);
+        const float x = fmaxf(x0, x1) * f[g];
+        top = fmaxf(top, x);
+        topv = fmaxf(topv, x + vl[g]);
       }
       const bool need = top > m + LAZY || topv > mv + LAZY;
       if (__any_sync(0xffffffffu, need)) {
@@ -1298,8 +1308,8 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
           const float c = sfu_exp2(vl[2 * half + g] + dv);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float e0 = sfu_exp2(__uint_as_float(v[half][16 * g + i]) - mm);
-            const float e1 = sfu_exp2(__uint_as_float(v[half][16 * g + i + 1]) - mm);
+            const float e0 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i]), f[2 * half + g], -mm));
+            const float e1 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i + 1]), f[2 * half + g], -mm));
             l += e0 + e1;
             pk[8 * g + i / 2] = pack_f16(e0 * c, e1 * c);
           }
@@ -1700,7 +1710,16 @@ bool launch_attn_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
 template <int HD>
 bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long row_tiles = ((long)a.max_new * at.G + CR - 1) / CR;
-  const int split = split_of(c, (long)a.S * a.H * row_tiles, 2, (max_len + CT - 1) / CT, 2);
+  // Blocks that have rows, about half a tile a sequence above the rows' own; two are resident an SM.  A block costs its
+  // tiles and about six more; blocks that do not fit at once cost a part of a wave beside their share.
+  const double tiles = (max_len + CT - 1) / CT, places = 2.0 * c.num_sms;
+  const double blocks = a.H * fmin((double)a.S * row_tiles, (double)a.n_rows * at.G / CR + 0.5 * a.S);
+  int split = 1;
+  double best = 0.0;
+  for (int i = 1; i <= 8 && (i == 1 || 2 * i <= tiles); i++) {
+    const double waves = blocks * i / places, cost = (waves <= 1.0 ? 1.0 : waves + 0.4) * (tiles / i + 6.0);
+    if (i == 1 || cost < best) best = cost, split = i;
+  }
   return launch_split<k_kv8_attn_tc<HD>>(c, a, at, split, row_tiles, C_THREADS, 1024 + TcShape<HD>::END + sizeof(TcShared));
 }
 
@@ -1712,7 +1731,11 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   constexpr int NS = HD == 32 ? 4 : 2;
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
   if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
-  if constexpr (sizeof(T) == 2) return launch_attn_tc<HD>(c, a, at, max_len);
+  // By trial: 20 to 48 rows of 64 or fewer dimensions take 10 to 25% less with the warp MMA's blocks of 64 rows; of 128
+  // dimensions, and from 64 rows on, tcgen05 takes less (64 rows 24.7 us against 27.9, 1000 rows half).
+  if constexpr (sizeof(T) == 2) {
+    if (HD == 128 || rows > 48) return launch_attn_tc<HD>(c, a, at, max_len);
+  }
   constexpr int TK = HD == 128 && sizeof(T) == 4 ? 32 : 64;
   return launch_attn_many<T, HD, TK, HD == 128 || sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
 }

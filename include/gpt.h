@@ -436,7 +436,8 @@ gpt_status gpt_sample_rows(const void* d_logits, int32_t logits_bf16, int32_t ro
  * one cache that write it are ordered by the caller.  Host errors come back as
  * gpt_status; what only the device sees (a block id outside the pool, tokens
  * past the capacity, bad offsets) is left out, never dereferenced, and sets a
- * GPT_FLAG_* bit in *d_flags, which the caller clears. */
+ * GPT_FLAG_* bit in *d_flags, which the caller clears (GPT_FLAG_TIMEOUT: a
+ * bounded wait ran out, the call's outputs are not valid). */
 typedef struct gpt_kv8_cache {
   int32_t n_seq;          /* sequences, at most 65535                               */
   int32_t n_head_kv;      /* key / value heads                                      */

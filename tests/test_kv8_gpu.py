@@ -221,6 +221,30 @@ def test_attention_blocks_of_rows(hd, P, H, G, lens, news, dtype):
     assert int(gpu.flags) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,news", [(64, 1, [1, 1]), (64, 2, [6, 3]), (64, 1, [30, 20]), (64, 1, [100, 60]), (128, 1, [60, 1]),
+                                       (32, 3, [40, 40])])
+def test_attention_scales_and_offsets(hd, G, news, dtype):
+    """A negative scale and a scale of 0 (every visible slot counts alike), rows of zeros, and q and out at an odd offset,
+    for every form of the kernel."""
+    lens = [70, 200]
+    gpu, ref, rng = make(19, [a + b for a, b in zip(lens, news)], 1, hd, 16)
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), G, hd, dtype)
+    q[-1] = 0
+    q64[-1] = 0
+    for scale in (-0.2, 0.0, 0.125):
+        out, lse, _ = check_attention(gpu, ref, q, q64, st, news, dtype, scale=scale)
+        wide = torch.full((2, q.shape[0], G * hd + 1), 5.0, dtype=q.dtype, device="cuda")
+        wide[0, :, 1:] = q.flatten(1)
+        at = wide[:, :, 1:].unflatten(2, (G, hd))
+        got_lse = torch.zeros_like(lse)
+        gpu.attention(at[0], at[1], start=dev(st), max_new=max(news), lse=got_lse, scale=scale)
+        assert torch.equal(at[1], out) and torch.equal(got_lse, lse) and (wide[1, :, 0] == 5.0).all()
+
+
 @pytest.mark.parametrize("max_len", [0, 1])
 def test_attention_blocks_of_rows_with_holes_and_nan(max_len):
     """Block ids outside the pool, and NaN in V, among many rows; a sequence none of whose blocks is in the pool."""
