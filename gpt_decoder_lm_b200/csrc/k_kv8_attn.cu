@@ -188,11 +188,13 @@ struct AttnArgs {
   float* lse;
 };
 
+constexpr int MAX_SPLIT = 16;  // blocks of a cluster
+
 // What a block has of its rows when it is done with its part of the slots.
 template <int ROWS>
 struct RowStats {
   float m[ROWS], mv[ROWS], l[ROWS];  // maxima and sum, as above
-  float fac[8][ROWS];                // for the join: each part's factor, then the row's
+  float fac[MAX_SPLIT][ROWS];        // for the join: each part's factor, then the row's
   float inv[ROWS], back[ROWS];
 };
 
@@ -205,22 +207,24 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
   const int G = at.G;
   if (n_split > 1) cl.sync(); else __syncthreads();
   for (int r = threadIdx.x; r < rows; r += THREADS) {
-    float km[8], kv[8], kl[8], mm = -INFINITY, mmv = -INFINITY, ll = 0.f;
+    float km[MAX_SPLIT], kv[MAX_SPLIT], kl[MAX_SPLIT], mm = -INFINITY, mmv = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      const bool on = k < n_split;
-      const RowStats<ROWS>* o = n_split > 1 ? cl.map_shared_rank(&st, on ? k : 0) : &st;
-      km[k] = on ? o->m[r] : -INFINITY;
-      kv[k] = on ? o->mv[r] : -INFINITY;
-      kl[k] = on ? o->l[r] : 0.f;
-    }
+    for (int k = 0; k < MAX_SPLIT; k++)
+      if (k < n_split) {
+        const RowStats<ROWS>* o = n_split > 1 ? cl.map_shared_rank(&st, k) : &st;
+        km[k] = o->m[r];
+        kv[k] = o->mv[r];
+        kl[k] = o->l[r];
+      }
 #pragma unroll
-    for (int k = 0; k < 8; k++) mm = fmaxf(mm, km[k]), mmv = fmaxf(mmv, kv[k]);
+    for (int k = 0; k < MAX_SPLIT; k++)
+      if (k < n_split) mm = fmaxf(mm, km[k]), mmv = fmaxf(mmv, kv[k]);
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      ll += km[k] == -INFINITY ? kl[k] : kl[k] * sfu_exp2(km[k] - mm);
-      st.fac[k][r] = kv[k] == -INFINITY ? 1.f : sfu_exp2(kv[k] - mmv);
-    }
+    for (int k = 0; k < MAX_SPLIT; k++)
+      if (k < n_split) {
+        ll += km[k] == -INFINITY ? kl[k] : kl[k] * sfu_exp2(km[k] - mm);
+        st.fac[k][r] = kv[k] == -INFINITY ? 1.f : sfu_exp2(kv[k] - mmv);
+      }
     // a row that sees nothing: zeros, and the log of an empty sum
     st.inv[r] = ll == 0.f ? 0.f : 1.f / ll;
     st.back[r] = ll == 0.f ? 0.f : exp2f(mmv - mm);
@@ -1665,16 +1669,20 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, Att
   }
 }
 
-// few blocks: the slots of each are split over a cluster of up to 8, each with `least` tiles or more
+// A cluster of 16 blocks needs as many SMs of one GPC: at most six such clusters are asked for (eight, 128 blocks, ran in
+// two waves: 36.6 us where clusters of 8 took 33.6).  More heads and sequences are split over at most 8.
+int widest(double blocks) { return blocks <= 6.0 ? MAX_SPLIT : 8; }
+
+// few blocks: the slots of each are split over a cluster, each with `least` tiles or more
 int split_of(const Ctx& c, long blocks, long resident, long tiles, long least) {
   const long want = (resident * c.num_sms + blocks - 1) / blocks, most = (tiles + least - 1) / least;
   const long split = want < most ? want : most;
-  return (int)(split < 1 ? 1 : split > 8 ? 8 : split);
+  return (int)(split < 1 ? 1 : split > widest(blocks) ? widest(blocks) : split);
 }
 
 template <auto Kernel>
 bool launch_split(Ctx& c, const Kv8Args& a, AttnArgs at, int split, long row_tiles, int threads, size_t smem) {
-  if (!allow_smem<Kernel>((int)smem)) return false;
+  if (!allow_smem<Kernel>((int)smem, split > 8)) return false;
   at.n_split = split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split * row_tiles), a.H, a.S);
@@ -1690,9 +1698,9 @@ bool launch_split(Ctx& c, const Kv8Args& a, AttnArgs at, int split, long row_til
   return cudaLaunchKernelEx(&cfg, Kernel, a, at) == cudaSuccess;
 }
 
-template <typename T, int HD, int NT, int NS, int MINB>
+template <typename T, int HD, int NT, int NS, int MINB, int NW = 4>
 bool launch_attn(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
-  constexpr int NW = 4, ROWS = 8 * NT;
+  constexpr int ROWS = 8 * NT;
   constexpr size_t ring = sizeof(Stage<HD>) * NW * NS, join = (size_t)(NW * ROWS * (HD + 4) + ROWS * HD) * 4;
   const long row_tiles = ((long)a.max_new * at.G + ROWS - 1) / ROWS;
   const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TT - 1) / TT, NW);
@@ -1716,7 +1724,7 @@ bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const double blocks = a.H * fmin((double)a.S * row_tiles, (double)a.n_rows * at.G / CR + 0.5 * a.S);
   int split = 1;
   double best = 0.0;
-  for (int i = 1; i <= 8 && (i == 1 || 2 * i <= tiles); i++) {
+  for (int i = 1; i <= widest((double)a.S * a.H * row_tiles) && (i == 1 || 2 * i <= tiles); i++) {
     const double waves = blocks * i / places, cost = (waves <= 1.0 ? 1.0 : waves + 0.4) * (tiles / i + 6.0);
     if (i == 1 || cost < best) best = cost, split = i;
   }
@@ -1729,6 +1737,9 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   // Stages a warp and blocks an SM, by trial: with 64 dimensions and 8 rows two stages and five blocks took 21.3 us for
   // 64 sequences of 12 heads, three and four 24.5 us.
   constexpr int NS = HD == 32 ? 4 : 2;
+  // heads and sequences that even clusters of 8 leave SMs without a block: eight warps a block
+  const long pairs = (long)a.S * a.H;
+  if (rows <= 8 && pairs * 8 <= c.num_sms) return launch_attn<T, HD, 1, NS, 1, 8>(c, a, at, max_len);
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
   if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
   // By trial: 20 to 48 rows of 64 or fewer dimensions take 10 to 25% less with the warp MMA's blocks of 64 rows; of 128

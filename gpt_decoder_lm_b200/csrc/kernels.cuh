@@ -18,17 +18,22 @@ struct Ctx {
   Timing* timing = nullptr;   // null when timing is off
 };
 
-// Lets kernel K have `bytes` of dynamic shared memory a block on the current device: asked of the driver once for each
-// device, not at every launch.
+// Lets kernel K have `bytes` of dynamic shared memory a block on the current device, and clusters of more than eight
+// blocks: asked of the driver once for each device, not at every launch.
 template <auto K>
-bool allow_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
+bool allow_smem(int bytes, bool wide_clusters = false) {
+  static std::atomic<uint64_t> done[2];  // a bit a device: shared memory, wide clusters
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (done.load(std::memory_order_acquire) & bit) return true;
-  if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  done.fetch_or(bit, std::memory_order_release);
+  if (!(done[0].load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done[0].fetch_or(bit, std::memory_order_release);
+  }
+  if (wide_clusters && !(done[1].load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+    done[1].fetch_or(bit, std::memory_order_release);
+  }
   return true;
 }
 
