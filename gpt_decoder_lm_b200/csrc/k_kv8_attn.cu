@@ -1669,9 +1669,8 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, Att
   }
 }
 
-// A cluster of 16 blocks needs as many SMs of one GPC: at most six such clusters are asked for (eight, 128 blocks, ran in
-// two waves: 36.6 us where clusters of 8 took 33.6).  More heads and sequences are split over at most 8.
-int widest(double blocks) { return blocks <= 6.0 ? MAX_SPLIT : 8; }
+// The widest cluster to be asked for.  More than 8 blocks, only for few clusters: see launch_split.
+int widest(double blocks) { return blocks <= 18.0 ? MAX_SPLIT : 8; }
 
 // few blocks: the slots of each are split over a cluster, each with `least` tiles or more
 int split_of(const Ctx& c, long blocks, long resident, long tiles, long least) {
@@ -1680,12 +1679,24 @@ int split_of(const Ctx& c, long blocks, long resident, long tiles, long least) {
   return (int)(split < 1 ? 1 : split > widest(blocks) ? widest(blocks) : split);
 }
 
+// How many clusters of `split` blocks the current device runs at once: asked of the driver once for each.
+template <auto Kernel>
+int active_clusters(int split, cudaLaunchConfig_t cfg) {
+  static std::atomic<int> known[8][MAX_SPLIT + 1];  // number + 1
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 8 && (n = known[dev][split].load(std::memory_order_relaxed)) > 0) return n - 1;
+  cfg.gridDim.x = split;
+  if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) return 0;
+  if (dev < 8) known[dev][split].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <auto Kernel>
 bool launch_split(Ctx& c, const Kv8Args& a, AttnArgs at, int split, long row_tiles, int threads, size_t smem) {
   if (!allow_smem<Kernel>((int)smem, split > 8)) return false;
-  at.n_split = split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(split * row_tiles), a.H, a.S);
+  cfg.gridDim = dim3(1, a.H, a.S);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
@@ -1695,6 +1706,11 @@ bool launch_split(Ctx& c, const Kv8Args& a, AttnArgs at, int split, long row_til
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // A cluster takes its SMs from one GPC, so that wide ones leave SMs over and may not all run at once: 8 heads of 128,
+  // 30000 slots, took 24.4 us in clusters of 10 and 41.5 us, in two waves, in clusters of 12.
+  for (; split > 8 && active_clusters<Kernel>(split, cfg) < a.S * a.H * row_tiles; split--) attr[0].val.clusterDim.x = split - 1;
+  at.n_split = split;
+  cfg.gridDim.x = (unsigned)(split * row_tiles);
   return cudaLaunchKernelEx(&cfg, Kernel, a, at) == cudaSuccess;
 }
 
