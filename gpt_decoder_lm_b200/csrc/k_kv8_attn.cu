@@ -282,8 +282,8 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
 // warps, then the cluster's blocks through distributed shared memory, are joined
 // at the end in a fixed order.
 //
-// B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 65.3 us, 87%
-// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 18.9
+// B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 66 us, 86%
+// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 19.0
 // us (8.6 us at the copy bandwidth): about 3 us pass before the first tile (start,
 // length, table, codes), a warp's tile of 32 slots takes some 540 cycles of its
 // scheduler (64 conversions at 2, 16 MMA at 12.5, the rest softmax), and SMs with
