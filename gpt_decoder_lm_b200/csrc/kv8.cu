@@ -37,12 +37,11 @@ using namespace gpt;
 
 // The step's rows.
 gpt_status row_args(const int32_t* d_start, int32_t n_rows, int32_t max_new, Kv8Args* a) {
-  if (n_rows < 1 || max_new < 1 || max_new > n_rows || (!d_start && (max_new != 1 || n_rows > a->S)))
-    return GPT_ERR_INVALID_ARG;
-  if (max_new > (1 << 30)) return GPT_ERR_UNSUPPORTED;
+  if (n_rows < 1 || max_new < 1 || (!d_start && (max_new != 1 || n_rows > a->S))) return GPT_ERR_INVALID_ARG;
   a->start = d_start;
   a->n_rows = n_rows;
-  a->max_new = max_new;
+  a->max_new = max_new < n_rows ? max_new : n_rows;  // a bound: no sequence has more rows than there are
+  if (a->max_new > (1 << 30)) return GPT_ERR_UNSUPPORTED;
   return GPT_OK;
 }
 
@@ -100,7 +99,7 @@ extern "C" gpt_status gpt_kv8_attention(const gpt_kv8_cache* cache, const int32_
       !rows_ok(d_out, out_ld, n_head, cache->head_dim, rows_bf16))
     return GPT_ERR_INVALID_ARG;
   const int G = n_head / a.H, cap = capacity(a);
-  if ((int64_t)max_new * G > (1 << 30)) return GPT_ERR_UNSUPPORTED;
+  if ((int64_t)a.max_new * G > (1 << 30)) return GPT_ERR_UNSUPPORTED;
   return launch(cuda_stream, [&](Ctx& c) {
     return kv8_attention(c, a, cache->head_dim, G, rows_bf16 != 0, d_q, q_ld, scale,
                          max_len == 0 || max_len > cap ? cap : max_len, d_out, out_ld, d_lse);
@@ -119,7 +118,7 @@ extern "C" gpt_status gpt_kv8_accumulate(const gpt_kv8_cache* cache, const int32
       !rows_ok(d_q, q_ld, n_head, cache->head_dim, rows_bf16))
     return GPT_ERR_INVALID_ARG;
   const int G = n_head / a.H, cap = capacity(a);
-  if ((int64_t)max_new * G > (1 << 30)) return GPT_ERR_UNSUPPORTED;
+  if ((int64_t)a.max_new * G > (1 << 30)) return GPT_ERR_UNSUPPORTED;
   return launch(cuda_stream, [&](Ctx& c) {
     return kv8_accumulate(c, a, cache->head_dim, G, rows_bf16 != 0, d_q, q_ld, scale,
                           max_len == 0 || max_len > cap ? cap : max_len, d_lse);

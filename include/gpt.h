@@ -426,8 +426,9 @@ gpt_status gpt_sample_rows(const void* d_logits, int32_t logits_bf16, int32_t ro
  *
  * The step's new tokens are the rows of packed arrays: sequence s has rows
  * d_start[s] .. d_start[s + 1] - 1 (device int32 [n_seq + 1]; at most max_new
- * rows each, none allowed, n_rows in all arrays); d_start NULL: one row for
- * each of the first n_rows <= n_seq sequences (max_new 1).  A row's heads are
+ * rows each, none allowed, n_rows in all arrays; max_new is a bound, which may
+ * be above n_rows); d_start NULL: one row for each of the first n_rows <= n_seq
+ * sequences (max_new 1).  A row's heads are
  * contiguous, rows ld elements apart; elements are bf16 (rows_bf16) or fp32.
  * Rows that belong to no sequence are neither read nor written.
  *

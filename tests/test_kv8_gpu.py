@@ -361,6 +361,27 @@ def test_bad_tables_and_offsets_are_left_out():
     assert int(gpu.flags) == gb.FLAG_CACHE_FULL and torch.equal(gpu.k, before)
 
 
+@pytest.mark.parametrize("n", [1, 5, 70])
+def test_bound_on_new_rows_above_the_rows(n):
+    """max_new is a bound: a caller's own, larger than all the rows of this step, changes nothing."""
+    results = []
+    for max_new in (n, 1000, 2 ** 31 - 1):
+        gpu, ref, rng = make(22, [40 + n], 2, 64, 16)
+        gpu.length.fill_(40)
+        q, _ = rows_of(rng, n, 4, 64, "bf16")
+        k, _ = rows_of(rng, n, 2, 64, "bf16")
+        out, lse, st = torch.zeros_like(q), torch.zeros(n, 4, device="cuda"), dev(starts([n]))
+        gpu.append(k, k, start=st, max_new=max_new)
+        gpu.attention(q, out, start=st, max_new=max_new, lse=lse)
+        gpu.accumulate(q, lse, start=st, max_new=max_new)
+        gpu.advance(start=st, n_rows=n, max_new=max_new)
+        results.append((gpu.k, gpu.v, gpu.k_scale, out, lse, gpu.weight, gpu.length))
+        assert int(gpu.flags) == 0 and int(gpu.length[0]) == 40 + n
+    for other in results[1:]:
+        for x, y in zip(results[0], other):
+            assert torch.equal(x.nan_to_num(), y.nan_to_num()) if x.is_floating_point() else torch.equal(x, y)
+
+
 def test_rows_behind_the_last_sequence_stay():
     gpu, ref, rng = make(16, [5, 9], 1, 64, 16)
     gpu.length.fill_(3)

@@ -54,7 +54,7 @@ def test_bad_caches_are_refused_by_every_call(lib, over, want):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(n_rows=0), dict(n_rows=3), dict(max_new=0), dict(max_new=2), dict(start=A, n_rows=4, max_new=5),
+    dict(n_rows=0), dict(n_rows=3), dict(max_new=0), dict(max_new=2), dict(start=A, n_rows=4, max_new=0),
     dict(k=None), dict(v=None), dict(k_ld=127), dict(v_ld=64), dict(k=A + 1), dict(v=A + 2, bf16=0)])
 def test_bad_rows_are_refused(lib, kw):
     assert append(lib, cache(), **kw) == "GPT_ERR_INVALID_ARG"
