@@ -59,6 +59,17 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The MMA cuts its sums off, which over hundreds of steps shows in fp32 (a long
+// context's outputs were off by 1e-5 of the largest).  fp32 rows let it add up
+// one step at a time and add the steps themselves, rounded to nearest.
+struct Exact {
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add_to(float (&d)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; i++) d[i] += x[i];
+  }
+};
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -143,9 +154,16 @@ struct QFrag {
       const uint32_t a0 = f16x2_e4m3(w0[ks]), a1 = f16x2_e4m3(w1[ks]);
       const uint32_t a2 = f16x2_e4m3(w0[ks] >> 16), a3 = f16x2_e4m3(w1[ks] >> 16);
 #pragma unroll
-      for (int nt = 0; nt < NT; nt++)
+      for (int nt = 0; nt < NT; nt++) {
+        if (TERMS == 1) {
+          mma(d[nt], a0, a1, a2, a3, b[0][nt][ks][0], b[0][nt][ks][1]);
+        } else {
+          Exact e;
 #pragma unroll
-        for (int m = 0; m < TERMS; m++) mma(d[nt], a0, a1, a2, a3, b[m][nt][ks][0], b[m][nt][ks][1]);
+          for (int m = TERMS - 1; m >= 0; m--) mma(e.x, a0, a1, a2, a3, b[m][nt][ks][0], b[m][nt][ks][1]);
+          e.add_to(d[nt]);
+        }
+      }
     }
   }
 };
@@ -567,9 +585,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
         for (int i = 0; i < 2; i++)
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
-            if (sizeof(T) == 4)  // fp32 outputs: the weights' second fp16 term
-              mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], plo[gr][nt][0], plo[gr][nt][1]);
+            if (sizeof(T) == 2) {
+              mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
+            } else {  // fp32 outputs: the weights' second fp16 term too
+              Exact e;
+              mma(e.x, aa[i][0], aa[i][1], aa[i][2], aa[i][3], plo[gr][nt][0], plo[gr][nt][1]);
+              mma(e.x, aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
+              e.add_to(o[2 * c + i][nt]);
+            }
           }
       }
     }
@@ -847,10 +870,18 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       for (int ks = 0; ks < KS; ks += 2) {
         uint32_t b[4];
         ldsm4(b, kb + k_off[ks / 2] + j * 16 * HD);
+        if (TERMS == 1) {
+          mma(sc[j], q[0][ks][0], q[0][ks][1], q[0][ks][2], q[0][ks][3], b[0], b[1]);
+          mma(sc[j], q[0][ks + 1][0], q[0][ks + 1][1], q[0][ks + 1][2], q[0][ks + 1][3], b[2], b[3]);
+        } else {
+          Exact e0, e1;
 #pragma unroll
-        for (int x = 0; x < TERMS; x++) {
-          mma(sc[j], q[x][ks][0], q[x][ks][1], q[x][ks][2], q[x][ks][3], b[0], b[1]);
-          mma(sc[j], q[x][ks + 1][0], q[x][ks + 1][1], q[x][ks + 1][2], q[x][ks + 1][3], b[2], b[3]);
+          for (int x = TERMS - 1; x >= 0; x--) {
+            mma(e0.x, q[x][ks][0], q[x][ks][1], q[x][ks][2], q[x][ks][3], b[0], b[1]);
+            mma(e1.x, q[x][ks + 1][0], q[x][ks + 1][1], q[x][ks + 1][2], q[x][ks + 1][3], b[2], b[3]);
+          }
+          e0.add_to(sc[j]);
+          e1.add_to(sc[j]);
         }
       }
     }
@@ -929,11 +960,17 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       for (int i = 0; i < HD / 8; i += 2) {
         uint32_t b[4];
         ldsm4t(b, vb + v_off[i / 2] + kk * 32 * HD);
-        mma(o[i], p[0], p[1], p[2], p[3], b[0], b[1]);
-        mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
-        if (TERMS == 2) {
-          mma(o[i], plo[0], plo[1], plo[2], plo[3], b[0], b[1]);
-          mma(o[i + 1], plo[0], plo[1], plo[2], plo[3], b[2], b[3]);
+        if (TERMS == 1) {
+          mma(o[i], p[0], p[1], p[2], p[3], b[0], b[1]);
+          mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
+        } else {
+          Exact e0, e1;
+          mma(e0.x, plo[0], plo[1], plo[2], plo[3], b[0], b[1]);
+          mma(e1.x, plo[0], plo[1], plo[2], plo[3], b[2], b[3]);
+          mma(e0.x, p[0], p[1], p[2], p[3], b[0], b[1]);
+          mma(e1.x, p[0], p[1], p[2], p[3], b[2], b[3]);
+          e0.add_to(o[i]);
+          e1.add_to(o[i + 1]);
         }
       }
     }
@@ -1520,8 +1557,16 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_many(Kv8Args a, At
             ldsm4(b, qb + term * TILE + q_off[k / 2] + nt * 16 * HD);
 #pragma unroll
             for (int x = 0; x < 2; x++) {
-              mma(d[x], ka[x][k][0], ka[x][k][1], ka[x][k][2], ka[x][k][3], b[0], b[1]);
-              mma(d[x], ka[x][k + 1][0], ka[x][k + 1][1], ka[x][k + 1][2], ka[x][k + 1][3], b[2], b[3]);
+              if (TERMS == 1) {
+                mma(d[x], ka[x][k][0], ka[x][k][1], ka[x][k][2], ka[x][k][3], b[0], b[1]);
+                mma(d[x], ka[x][k + 1][0], ka[x][k + 1][1], ka[x][k + 1][2], ka[x][k + 1][3], b[2], b[3]);
+              } else {
+                Exact e0, e1;
+                mma(e0.x, ka[x][k][0], ka[x][k][1], ka[x][k][2], ka[x][k][3], b[0], b[1]);
+                mma(e1.x, ka[x][k + 1][0], ka[x][k + 1][1], ka[x][k + 1][2], ka[x][k + 1][3], b[2], b[3]);
+                e0.add_to(d[x]);
+                e1.add_to(d[x]);
+              }
             }
           }
 #pragma unroll

@@ -281,6 +281,35 @@ def test_attention_splits_agree_with_the_oracle():
         check_attention(gpu, ref, q, q64, starts([1]), [1], "fp32", max_len=max_len)
 
 
+@pytest.mark.parametrize("n,hd,P", [(1, 64, 16), (9, 128, 64), (40, 32, 16)])
+def test_long_contexts_in_fp32(n, hd, P):
+    """Over 20,000 slots fp32 outputs stay at fp32's accuracy.  Per weight: the score's error, 2^-23 of sum |q k| (q as
+    two fp16 terms) and 2^-24 for each of the sums' steps, the exponential's 2^-22 and the weight's 2^-22; these are
+    independent from slot to slot, as are the values, so that they stand to the output as to a weight: with sum |q k|
+    about 8 and 8 steps below 2e-6 (a sum that is cut off, not rounded, at each of its steps leaves 7e-6)."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    len_ = 20000
+    blocks = -(-(len_ + n) // P)
+    c = gb.KV8Cache.allocate(1, 1, hd, P, blocks)
+    k = torch.randn(len_ + n, 1, hd, device="cuda", generator=gen)
+    v = torch.randn(len_ + n, 1, hd, device="cuda", generator=gen)
+    at = dev(starts([len_ + n]))
+    c.append(k, v, start=at, max_new=len_ + n)
+    c.length.fill_(len_)
+    q = torch.randn(n, 2, hd, device="cuda", generator=gen)
+    out, lse = torch.zeros_like(q), torch.zeros(n, 2, device="cuda")
+    c.attention(q, out, start=dev(starts([n])), max_new=n, lse=lse)
+
+    def values(codes, scale):
+        x = codes.view(torch.float8_e4m3fn).double() * scale.double()[:, :, None, None]
+        return x.transpose(0, 1).reshape(-1, hd)[:len_ + n]
+    z = torch.einsum("ihd,jd->ihj", q.double(), values(c.k, c.k_scale)) * hd ** -0.5
+    z.masked_fill_((torch.arange(len_ + n, device="cuda") > len_ + torch.arange(n, device="cuda")[:, None])[:, None], -np.inf)
+    want = torch.softmax(z, -1) @ values(c.v, c.v_scale)
+    assert float((out.double() - want).norm() / want.norm()) <= 2e-6
+    assert float((lse.double() - torch.logsumexp(z, -1)).abs().max()) <= 4e-6
+
+
 def test_attention_scale_ranges():
     """Blocks whose value scales are far apart, and where the large weight sits on the small values."""
     gpu, ref, rng = make(13, [64], 1, 64, 16, spread=False)
