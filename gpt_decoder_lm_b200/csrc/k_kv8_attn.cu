@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
 // (43 us with 16 rows a block and the conversions in every warp).  A warp's tile
 // of 64 slots is 64 MMA at 12.5 cycles; three blocks an SM keep the pipe 80% busy
 // between a prologue and a join of together a third of a block's time.
-constexpr int MR = 64, MW = 4;  // rows and warps of a block
+constexpr int MR = 64, MW = 4, MT = 64;  // rows and warps of a block, slots of a tile
 
 template <int HD>
 __device__ __forceinline__ uint32_t half_at(int row, int chunk) {  // byte offset of 16 bytes of a tile of fp16 rows
@@ -690,20 +690,20 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
                : "r"(at));
 }
 
-template <int HD, int TK>
+template <int HD>
 struct alignas(16) HalfTile {
-  uint8_t k[TK * HD * 2];
-  uint8_t v[TK * HD * 2];
+  uint8_t k[MT * HD * 2];
+  uint8_t v[MT * HD * 2];
 };
 
-template <typename T, int HD, int TK, int MINB>
+template <typename T, int HD, int MINB>
 __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, AttnArgs at) {
-  constexpr int KS = HD / 16, NG = TK / 16, TERMS = sizeof(T) == 4 ? 2 : 1;
-  constexpr int CPR = HD / 16, CPT = TK * CPR / (MW * 32);  // 16-code chunks a row; of K, and of V, a thread
+  constexpr int KS = HD / 16, NG = MT / 16, TERMS = sizeof(T) == 4 ? 2 : 1;
+  constexpr int CPR = HD / 16, CPT = MT * CPR / (MW * 32);  // 16-code chunks a row; of K, and of V, a thread
   constexpr int OP = HD + 4;
   static_assert(CPT >= 1, "a thread has a chunk");
   extern __shared__ __align__(16) uint8_t smem[];
-  HalfTile<HD, TK>* tile_mem = reinterpret_cast<HalfTile<HD, TK>*>(smem);
+  HalfTile<HD>* tile_mem = reinterpret_cast<HalfTile<HD>*>(smem);
   __shared__ float g_ks[2][NG], g_v[2][NG];  // the groups' K scales and log2 V scales (-infinity: no block)
   __shared__ RowStats<MR> stats;
 
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   const int wrow = row0 + 16 * w;  // the warp's rows
   const int w_lo = min(len + min(R - 1, wrow) / G + 1, cap), w_hi = min(len + min(R - 1, wrow + 15) / G + 1, cap);
 
-  const int tiles = (see_hi + TK - 1) / TK;
+  const int tiles = (see_hi + MT - 1) / MT;
   const int per = (tiles + n_split - 1) / n_split;
   const int t0 = min(tiles, split * per), t1 = min(tiles, t0 + per);
 
@@ -733,19 +733,19 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   auto look = [&](int tile) {
 #pragma unroll
     for (int u = 0; u < CPT; u++) {
-      const int j = tile * TK + trow + u * (MW * 32 / CPR);
+      const int j = tile * MT + trow + u * (MW * 32 / CPR);
       blk[u] = -1;
       if (tile < t1 && j < see_hi) blk[u] = ids[j >> a.lgP];  // first touched when the tile is fetched
     }
     gblk = -1;
-    if (tid < NG && tile < t1 && tile * TK + tid * 16 < see_hi) gblk = ids[(tile * TK + tid * 16) >> a.lgP];
+    if (tid < NG && tile < t1 && tile * MT + tid * 16 < see_hi) gblk = ids[(tile * MT + tid * 16) >> a.lgP];
   };
   auto fetch = [&](int tile) {
 #pragma unroll
     for (int u = 0; u < CPT; u++) {
       ck[u] = cv[u] = make_uint4(0, 0, 0, 0);
       if ((unsigned)blk[u] < (unsigned)a.n_blocks) {
-        const int j = tile * TK + trow + u * (MW * 32 / CPR);
+        const int j = tile * MT + trow + u * (MW * 32 / CPR);
         const size_t src = ((((size_t)blk[u] * a.H + h) << a.lgP) + (j & (a.P - 1))) * HD + (tid % CPR) * 16;
         ck[u] = *reinterpret_cast<const uint4*>(a.k + src);
         cv[u] = *reinterpret_cast<const uint4*>(a.v + src);
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     }
     if (tid < NG && tile < t1) {
       const bool on = (unsigned)gblk < (unsigned)a.n_blocks;
-      if (!on && tile * TK + tid * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
+      if (!on && tile * MT + tid * 16 < see_hi) kv8_flag(a, FLAG_BLOCK);
       const size_t bh = (size_t)(on ? gblk : 0) * a.H + h;
       gks = gvs = 0.f;
       if (on) gks = a.ks[bh], gvs = a.vs[bh];
@@ -763,8 +763,8 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   // that not every row sees whole it is taken out of V.  True where that happened.
   auto convert = [&](int tile, int buf) -> bool {
     bool nan = false;
-    const bool partial = tile * TK + TK > see_lo && see_lo != see_hi;
-    HalfTile<HD, TK>& m = tile_mem[buf];
+    const bool partial = tile * MT + MT > see_lo && see_lo != see_hi;
+    HalfTile<HD>& m = tile_mem[buf];
 #pragma unroll
     for (int u = 0; u < CPT; u++) {
       const int i = u * MW * 32 + tid, row = i / CPR, ch = 2 * (i % CPR);
@@ -858,13 +858,13 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     const bool poison = __syncthreads_or(convert(tile, buf));
     fetch(tile + 1);
     look(tile + 2);
-    if (wrow >= R || tile * TK >= w_hi) continue;  // nothing that the warp's rows see
+    if (wrow >= R || tile * MT >= w_hi) continue;  // nothing that the warp's rows see
     const uint32_t kb = (uint32_t)__cvta_generic_to_shared(tile_mem[buf].k), vb = (uint32_t)__cvta_generic_to_shared(tile_mem[buf].v);
 
     // ---- scores: [8 tokens][row half, token parity]
-    float sc[TK / 8][4];
+    float sc[MT / 8][4];
 #pragma unroll
-    for (int j = 0; j < TK / 8; j++) {
+    for (int j = 0; j < MT / 8; j++) {
       sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ks += 2) {
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       }
     }
     float vl[NG], top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-    bool all = tile * TK + TK <= w_lo;
+    bool all = tile * MT + MT <= w_lo;
 #pragma unroll
     for (int gr = 0; gr < NG; gr++) {
       vl[gr] = g_v[buf][gr];
@@ -899,10 +899,10 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     }
     if (!all) {
 #pragma unroll
-      for (int j = 0; j < TK / 8; j++)
+      for (int j = 0; j < MT / 8; j++)
 #pragma unroll
         for (int y = 0; y < 4; y++)
-          if (tile * TK + 8 * j + 2 * t + (y & 1) >= see[y >> 1] || vl[j / 2] == -INFINITY) sc[j][y] = -INFINITY;
+          if (tile * MT + 8 * j + 2 * t + (y & 1) >= see[y >> 1] || vl[j / 2] == -INFINITY) sc[j][y] = -INFINITY;
     }
     bool grow = false;
 #pragma unroll
@@ -975,8 +975,8 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       }
     }
     if (poison) {  // the NaN that were taken out go into the rows that see them
-      for (int row = 0; row < TK; row++) {
-        const int j = tile * TK + row;
+      for (int row = 0; row < MT; row++) {
+        const int j = tile * MT + row;
         if (j >= see_hi) break;
         const int b = ids[j >> a.lgP];
         if ((unsigned)b >= (unsigned)a.n_blocks) continue;
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   join_blocks<T, HD, MR, OP, MW * 32>(stats, part, n_split, split, min(MR, R - row0), at, r0, row0, h, a.H * G);
 }
 
-// ---------------------------------------------------------------- many rows of bf16: tcgen05
+// ---------------------------------------------------------------- many rows: tcgen05
 //
 // 128 rows of one key / value head and sequence over one of the cluster's equal
 // parts of the slots, 64 slots a tile.  Two warps turn codes into fp16 tiles
@@ -1019,23 +1019,34 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // fp16 over its scores, and O is rescaled in TMEM only where a running maximum
 // has to grow.  Statistics and joins are those of k_kv8_attn.
 //
+// fp32 rows: Q and P are two fp16 terms each, and the products of four tiles at a
+// time are added to sums of their own (FLUSH): 6e-7 of the outputs' norm over
+// 20,000 slots, where sums left in the tensor core drift off by 2.7e-6.
+//
 // B200: 2 sequences of 900 to 1000 new rows over 3000 to 4000 slots, 16 heads of
 // 64: 100 us, 310 TFLOP/s of the visible products (the warp MMA's blocks of 64
 // rows: 203 us).  Two resident blocks keep the SFU and the schedulers of the
 // softmax warps busy: a tile is 8192 exponentials at 16 a cycle and SM, and about
 // five other instructions each.  63 to 200 new rows over up to 1501 slots, 4
 // sequences of 25 heads: 28 us (33 us), two fifths of it before the first tile
-// and in the join.
+// and in the join.  fp32, 3 sequences of 71 new rows over 4300 slots, 8 heads of
+// 128: 67 us (the warp MMA's blocks: 100 us).
 constexpr int CR = 128, CT = 64;             // rows of a block, slots of a tile
 constexpr int C_SOFT = 4, C_MAKE = 2;        // softmax and converting warps; one more issues
 constexpr int C_THREADS = (C_SOFT + 1 + C_MAKE) * 32;
 
-template <int HD>
+template <typename T, int HD>
 struct TcShape {
+  static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;                  // fp16 terms of Q and P
+  static constexpr int MINB = TERMS == 2 && HD == 128 ? 1 : 2;          // blocks an SM
+  // fp32 rows: the products add up over FLUSH tiles only; then they are added, rounded to nearest, to the sums so far,
+  // which have their own columns (the tensor core cuts its sums off: over hundreds of tiles that shows in fp32)
+  static constexpr int FLUSH = TERMS == 2 ? 4 : 1 << 30, SUMS = 128 + (HD == 128 ? 128 : 64);
+  static constexpr int COLS = TERMS == 2 && HD == 128 ? 512 : 256;      // TMEM columns
   static constexpr int NB = HD == 128 ? 2 : 1, WD = HD < 64 ? HD : 64;  // blocks of 64 dimensions, dimensions a block
   static constexpr int NS = HD == 128 ? 2 : 3;                          // stages
   static constexpr int QB = CR * 128, TB = CT * 128;                    // bytes of a block's Q, and of K or V
-  static constexpr int KV = NB * QB, STAGE = 2 * NB * TB;               // the first stage; K blocks, then V blocks
+  static constexpr int KV = TERMS * NB * QB, STAGE = 2 * NB * TB;       // the first stage; K blocks, then V blocks
   static constexpr int END = KV + NS * STAGE, PITCH = HD + 4;           // (later: outputs [CR][PITCH])
   static_assert(CR * PITCH * 4 <= END, "the outputs take the tiles' place");
 };
@@ -1048,9 +1059,9 @@ struct TcShared {
   int abort;
 };
 
-template <int HD>
-__global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
-  using S = TcShape<HD>;
+template <typename T, int HD>
+__global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
+  using S = TcShape<T, HD>;
   using namespace sm100;
   constexpr int CPR = HD / 16, CPT = (CT * CPR + C_MAKE * 32 - 1) / (C_MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
   extern __shared__ uint8_t raw_smem[];
@@ -1092,7 +1103,7 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
     fence_barrier_init();
   }
   if (warp == C_SOFT) {
-    tmem_alloc(smem_u32(&sh.tmem), 256);
+    tmem_alloc(smem_u32(&sh.tmem), S::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -1204,9 +1215,11 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
 #pragma unroll
         for (int nb = 0; nb < S::NB; nb++)
 #pragma unroll
-          for (int kk = 0; kk < CT / 16; kk++)
-            mma_bf16_ts(tmem + 128 + 64 * nb, tmem + 64 * u + 8 * kk, desc_sw128(v + nb * S::TB + kk * 2048, S::TB, 1024), id_o,
-                        (i > 0 || kk > 0) ? 1u : 0u);
+          for (int x = S::TERMS - 1; x >= 0; x--)
+#pragma unroll
+            for (int kk = 0; kk < CT / 16; kk++)
+              mma_bf16_ts(tmem + 128 + 64 * nb, tmem + 64 * u + 32 * x + 8 * kk, desc_sw128(v + nb * S::TB + kk * 2048, S::TB, 1024),
+                          id_o, ((S::TERMS == 2 ? i % S::FLUSH : i) > 0 || kk > 0 || x < S::TERMS - 1) ? 1u : 0u);
         mma_commit(pv_done0 + 8 * u);
         mma_commit(kv_empty0 + 8 * (i % S::NS));
         return true;
@@ -1218,11 +1231,13 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
         // S[j & 1] is free: its previous tile's P (j - 2) was waited for below
         const uint32_t k = sb + S::KV + st * S::STAGE;
 #pragma unroll
-        for (int nb = 0; nb < S::NB; nb++)
+        for (int x = S::TERMS - 1; x >= 0; x--)
 #pragma unroll
-          for (int kk = 0; kk < S::WD / 16; kk++)
-            mma_bf16_ss(tmem + 64 * (j & 1), desc_sw128(sb + nb * S::QB + kk * 32, 16, 1024),
-                        desc_sw128(k + nb * S::TB + kk * 32, 16, 1024), id_s, nb > 0 || kk > 0);
+          for (int nb = 0; nb < S::NB; nb++)
+#pragma unroll
+            for (int kk = 0; kk < S::WD / 16; kk++)
+              mma_bf16_ss(tmem + 64 * (j & 1), desc_sw128(sb + (x * S::NB + nb) * S::QB + kk * 32, 16, 1024),
+                          desc_sw128(k + nb * S::TB + kk * 32, 16, 1024), id_s, x < S::TERMS - 1 || nb > 0 || kk > 0);
         mma_commit(s_full0 + 8 * (j & 1));
         if (j >= 1 && !(ok = issue_pv(j - 1))) break;
       }
@@ -1237,41 +1252,40 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
     float qf = 0.f;
     if (nt > 0) {
       // fp16 after a power of two, as in QFrag
-      const bf16* p = reinterpret_cast<const bf16*>(at.q) + (on ? (long)(r0 + rr / G) * at.q_ld + (long)(h * G + rr % G) * HD : 0);
+      const T* p = reinterpret_cast<const T*>(at.q) + (on ? (long)(r0 + rr / G) * at.q_ld + (long)(h * G + rr % G) * HD : 0);
       const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-      uint4 x[HD / 8];
+      constexpr int EV = 16 / sizeof(T);  // elements of a 16-byte load
+      alignas(16) T x[HD];
 #pragma unroll
-      for (int i = 0; i < HD / 8; i++) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (on) {
-          if (vec) {
-            x[i] = reinterpret_cast<const uint4*>(p)[i];
-          } else {
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(p) + 8 * i;
-            x[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
-                              e[6] | (uint32_t)e[7] << 16);
-          }
+      for (int i = 0; i < HD; i += EV) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on && vec) v = *reinterpret_cast<const uint4*>(p + i);
+        *reinterpret_cast<uint4*>(x + i) = v;
+        if (on && !vec) {
+#pragma unroll
+          for (int e = 0; e < EV; e++) x[i + e] = p[i + e];
         }
       }
-      uint32_t top = 0;
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < HD / 8; i++) {
-        const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                    __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-        top = max(top, max(m << 16, m & 0xffff0000u));
-      }
-      int e = top != 0 && top < 0x7f800000u ? 14 - ((int)(top >> 23) - 127) : 0;
+      for (int i = 0; i < HD; i++) top = fmaxf(top, fabsf(to_f<T>(x[i])));
+      int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
       e = min(max(e, -100), 100);
       // a factor of the scores that is positive: the scale's sign goes with the row
       const float up = copysignf(kv8_pow2(e), at.scale);
       qf = fmaxf(kv8_pow2(-e) * fabsf(at.scale) * 1.4426950408889634f, 1e-36f);
 #pragma unroll
-      for (int i = 0; i < HD / 8; i++) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t f[4];
+      for (int i = 0; i < HD; i += 8) {
+        uint32_t f[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) f[j] = pack_f16(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-        *reinterpret_cast<uint4*>(smem + (i / 8) * S::QB + half_at<64>(r, i % 8)) = make_uint4(f[0], f[1], f[2], f[3]);
+        for (int w = 0; w < 4; w++) {
+          const float x0 = to_f<T>(x[i + 2 * w]) * up, x1 = to_f<T>(x[i + 2 * w + 1]) * up;
+          f[w] = pack_f16(x0, x1);
+          if (S::TERMS == 2) lo[w] = pack_rest(x0, x1, f[w]);
+        }
+        uint8_t* to = smem + (i / 64) * S::QB + half_at<64>(r, i % 64 / 8);
+        *reinterpret_cast<uint4*>(to) = make_uint4(f[0], f[1], f[2], f[3]);
+        if (S::TERMS == 2) *reinterpret_cast<uint4*>(to + S::NB * S::QB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1338,12 +1352,41 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
             for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
             tmem_st_32x32b_x16(trow + 128 + c, o);
           }
+          if (S::TERMS == 2 && j > S::FLUSH) {  // the sums of earlier tiles
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(trow + S::SUMS + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+              tmem_st_32x32b_x16(trow + S::SUMS + c, o);
+            }
+          }
+          tmem_st_wait();
         }
+      }
+      if (S::TERMS == 2 && j > 0 && j % S::FLUSH == 0) {
+        if (!(ok = mbar_wait(pv_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag, gflags))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < HD; c += 16) {
+          uint32_t o[16], q[16];
+          tmem_ld_32x32b_x16(trow + 128 + c, o);
+          if (j > S::FLUSH) tmem_ld_32x32b_x16(trow + S::SUMS + c, q);
+          tmem_ld_wait();
+          if (j > S::FLUSH) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(q[i]));
+          }
+          tmem_st_32x32b_x16(trow + S::SUMS + c, o);
+        }
+        tmem_st_wait();
       }
       const float mm = m == -INFINITY ? 0.f : m, dv = mm - (mv == -INFINITY ? 0.f : mv);
 #pragma unroll
       for (int half = 0; half < 2; half++) {
-        uint32_t pk[16];
+        uint32_t pk[16], pl[16];
 #pragma unroll
         for (int g = 0; g < 2; g++) {
           const float c = sfu_exp2(vl[2 * half + g] + dv);
@@ -1353,10 +1396,12 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
             const float e1 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i + 1]), f[2 * half + g], -mm));
             l += e0 + e1;
             pk[8 * g + i / 2] = pack_f16(e0 * c, e1 * c);
+            if (S::TERMS == 2) pl[8 * g + i / 2] = pack_rest(e0 * c, e1 * c, pk[8 * g + i / 2]);
           }
         }
-        // over the scores, which have been read: the A operand of P V
+        // over the scores, which have been read: the A operand of P V (fp32 rows: its second terms behind it)
         tmem_st_32x32b_x16(trow + 64 * u + 16 * half, pk);
+        if (S::TERMS == 2) tmem_st_32x32b_x16(trow + 64 * u + 32 + 16 * half, pl);
       }
       tmem_st_wait();
       if (sh.nan[st][0] | sh.nan[st][1]) {
@@ -1387,6 +1432,13 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
       if (nt > 0) {  // (the same for all threads)
         tmem_ld_32x32b_x16(trow + 128 + c, o);
         tmem_ld_wait();
+        if (S::TERMS == 2 && nt > S::FLUSH) {
+          uint32_t q[16];
+          tmem_ld_32x32b_x16(trow + S::SUMS + c, q);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(q[i]));
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; i++)
@@ -1400,8 +1452,8 @@ __global__ void __launch_bounds__(C_THREADS, 2) k_kv8_attn_tc(Kv8Args a, AttnArg
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == C_SOFT) tmem_dealloc(tmem, 256);
-  join_blocks<bf16, HD, CR, S::PITCH, C_THREADS>(sh.stats, reinterpret_cast<float*>(smem), n_split, split, min(CR, R - row0), at,
+  if (warp == C_SOFT) tmem_dealloc(tmem, S::COLS);
+  join_blocks<T, HD, CR, S::PITCH, C_THREADS>(sh.stats, reinterpret_cast<float*>(smem), n_split, split, min(CR, R - row0), at,
                                                  r0, row0, h, a.H * G);
 }
 
@@ -1768,20 +1820,20 @@ bool launch_attn(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   return launch_split<k_kv8_attn<T, HD, NT, NW, NS, MINB>>(c, a, at, split, row_tiles, NW * 32, ring > join ? ring : join);
 }
 
-template <typename T, int HD, int TK, int MINB>
+template <typename T, int HD, int MINB>
 bool launch_attn_many(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
-  constexpr size_t tiles = sizeof(HalfTile<HD, TK>) * 2, join = (size_t)MR * (HD + 4) * 4;
+  constexpr size_t tiles = sizeof(HalfTile<HD>) * 2, join = (size_t)MR * (HD + 4) * 4;
   const long row_tiles = ((long)a.max_new * at.G + MR - 1) / MR;
-  const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + TK - 1) / TK, 2);
-  return launch_split<k_kv8_attn_many<T, HD, TK, MINB>>(c, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
+  const int split = split_of(c, (long)a.S * a.H * row_tiles, MINB, (max_len + MT - 1) / MT, 2);
+  return launch_split<k_kv8_attn_many<T, HD, MINB>>(c, a, at, split, row_tiles, MW * 32, tiles > join ? tiles : join);
 }
 
-template <int HD>
+template <typename T, int HD>
 bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
   const long row_tiles = ((long)a.max_new * at.G + CR - 1) / CR;
   // Blocks that have rows, about half a tile a sequence above the rows' own; two are resident an SM.  A block costs its
   // tiles and about six more; blocks that do not fit at once cost a part of a wave beside their share.
-  const double tiles = (max_len + CT - 1) / CT, places = 2.0 * c.num_sms;
+  const double tiles = (max_len + CT - 1) / CT, places = (double)TcShape<T, HD>::MINB * c.num_sms;
   const double blocks = a.H * fmin((double)a.S * row_tiles, (double)a.n_rows * at.G / CR + 0.5 * a.S);
   int split = 1;
   double best = 0.0;
@@ -1789,7 +1841,7 @@ bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
     const double waves = blocks * i / places, cost = (waves <= 1.0 ? 1.0 : waves + 0.4) * (tiles / i + 6.0);
     if (i == 1 || cost < best) best = cost, split = i;
   }
-  return launch_split<k_kv8_attn_tc<HD>>(c, a, at, split, row_tiles, C_THREADS, 1024 + TcShape<HD>::END + sizeof(TcShared));
+  return launch_split<k_kv8_attn_tc<T, HD>>(c, a, at, split, row_tiles, C_THREADS, 1024 + TcShape<T, HD>::END + sizeof(TcShared));
 }
 
 template <typename T, int HD>
@@ -1803,13 +1855,15 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   if (rows <= 8 && pairs * 8 <= c.num_sms) return launch_attn<T, HD, 1, NS, 1, 8>(c, a, at, max_len);
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
   if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
-  // By trial: 20 to 48 rows of 64 or fewer dimensions take 10 to 25% less with the warp MMA's blocks of 64 rows; of 128
-  // dimensions, and from 64 rows on, tcgen05 takes less (64 rows 24.7 us against 27.9, 1000 rows half).
-  if constexpr (sizeof(T) == 2) {
-    if (HD == 128 || rows > 48) return launch_attn_tc<HD>(c, a, at, max_len);
+  // By trial: 20 to 48 rows (fp32: 64, one block) of 64 or fewer dimensions take up to 25% less with the warp MMA's blocks
+  // of 64 rows; of 128 dimensions, and above, tcgen05 takes less (bf16: 64 rows 24.7 us against 27.9, 1000 rows half;
+  // fp32: 100 rows of 30 sequences 65.9 us against 90.1, 71 rows of 128 dimensions 67 against 100).
+  if constexpr (HD == 128) {
+    return launch_attn_tc<T, HD>(c, a, at, max_len);
+  } else {
+    if (rows > (sizeof(T) == 4 ? 64 : 48)) return launch_attn_tc<T, HD>(c, a, at, max_len);
+    return launch_attn_many<T, HD, sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
   }
-  constexpr int TK = HD == 128 && sizeof(T) == 4 ? 32 : 64;
-  return launch_attn_many<T, HD, TK, HD == 128 || sizeof(T) == 4 ? 2 : 3>(c, a, at, max_len);
 }
 
 template <typename T, int HD>

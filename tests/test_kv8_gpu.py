@@ -271,6 +271,36 @@ def test_attention_blocks_of_rows_with_holes_and_nan(max_len):
     assert torch.equal(torch.isnan(out), want)
 
 
+@pytest.mark.parametrize("max_len", [0, 1])
+@pytest.mark.parametrize("hd,G,n", [(128, 1, 20), (128, 2, 70), (64, 1, 100), (32, 5, 30)])
+def test_attention_sums_of_tiles_in_fp32(hd, G, n, max_len):
+    """Lengths around multiples of the slots between which fp32 sums are set aside, with running maxima that grow from
+    tile to tile, so that what was set aside is scaled too; one sequence sees holes and one NaN."""
+    lens = [64 * tiles + d for tiles in (3, 4, 5, 8, 9, 13) for d in (-1, 0, 1)]
+    gpu, ref, rng = make(29, [m + n for m in lens], 1, hd, 16)
+    for s in range(len(lens)):
+        for b in range(ref.table.shape[1]):
+            ref.ks[ref.table[s, b], 0] = 2.0 ** (b // 8 - 11)
+    gpu.k_scale.copy_(torch.from_numpy(ref.ks.astype(np.float32)))
+    table = ref.table.copy()
+    table[4, [0, 5, 17]] = [-1, ref.k.shape[0], 2 ** 31 - 1]
+    ref.table = table
+    gpu.table = torch.from_numpy(table).cuda()
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    news = [n] * len(lens)
+    st = starts(news)
+    q, q64 = rows_of(rng, n * len(lens), G, hd, "fp32")
+    out, lse, _ = check_attention(gpu, ref, q, q64, st, news, "fp32", max_len=max_len)
+    assert torch.isfinite(out).all() and int(gpu.flags) == gb.FLAG_BLOCK_RANGE
+    gpu.v[int(table[-1, 3]), 0, 7, 9] = 0x7F  # slot 55 of the last sequence, which all its rows see
+    again = torch.zeros_like(out)
+    gpu.attention(q, again, start=dev(st), max_new=n, max_len=max_len)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[-n:, :, 9] = True
+    assert torch.equal(torch.isnan(again), want) and torch.equal(again[~want], out[~want])
+
+
 def test_attention_splits_agree_with_the_oracle():
     """One sequence, long enough to be split over a cluster's blocks; the bound on the length decides how."""
     gpu, ref, rng = make(12, [5001], 1, 64, 16)
