@@ -79,12 +79,21 @@ struct RowArgs {
 
 // The row's scale: distances from its largest logit, in log2 of probability.
 struct Scale {
-  float zf, cf;   // the largest logit; 32 log2(e) / temperature
+  float zf, cf;   // the largest logit; 32 log2(e) / temperature, divided by `half`
+  float half;     // 1, or 1/2 where a distance that counts may pass fp32's range
   double cd;      // log2(e) / temperature
+  __device__ __forceinline__ void set(float top, float temperature) {
+    zf = top;
+    cd = 1.4426950408889634074 / (double)temperature;
+    half = 48.0 / cd < 1.7e38 ? 1.f : 0.5f;  // (cd may be 0)
+    cf = fminf((float)(cd * 32.0 / half), 3.0e38f);
+  }
   __device__ __forceinline__ double dist(float z) const { return ((double)zf - (double)z) * cd; }
-  // rint(32 y) in fp32; both roundings keep the order of logits.  *fr: 32 y - bin
+  // rint(32 y) in fp32, of a logit not below floor(48); both roundings keep the order of logits.  *fr: 32 y - bin.
+  // half * (zf - z), in one rounding: with temperatures of 1e37 and more (infinity included) logits as far apart as
+  // fp32 allows have weights, and their distance itself would be infinite, its bin outside the histogram.
   __device__ __forceinline__ int bin(float z, float* fr = nullptr) const {
-    const float d = zf - z;
+    const float d = fmaf(-half, z, half * zf);
     const float t = fmaf(d, cf, 12582912.f);
     if (fr) *fr = fmaf(d, cf, 12582912.f - t);
     return __float_as_int(t) - 0x4b400000;
@@ -333,9 +342,7 @@ __global__ void __launch_bounds__(NT, 2) k_sample_rows(RowArgs a) {
     top = 0.f;
   }
   Scale sc;
-  sc.zf = top;
-  sc.cd = 1.4426950408889634074 / (double)temp;
-  sc.cf = fminf((float)sc.cd * 32.f, 3.0e38f);
+  sc.set(top, temp);
 
   // the lowest logit that is kept: a token below 2^-48 of the largest has no weight
   float lo = sc.floor(48.0);

@@ -171,3 +171,21 @@ def test_captured_and_on_another_stream():
             gb.sample_rows(z, u, out, top_p=tp, logp=lp)
         s.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lp, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [700, 3001, 20011])
+def test_temperatures_at_which_the_whole_range_of_logits_counts(V, dtype):
+    """Logits as far apart as the type allows (their distance is beyond fp32), at temperatures, infinity among them,
+    where all of them or most have weight, under each filter."""
+    rng = np.random.default_rng(V)
+    rows = 12
+    z = (rng.uniform(-1, 1, (rows, V)) * 3.38e38).astype(np.float32)
+    z[:, 0], z[:, V // 2] = 3.38e38, -3.38e38
+    z[1, 5], z[2, 7:20], z[3, 9] = np.inf, -np.inf, np.nan
+    z = torch.from_numpy(z).to(DT[dtype]).cuda()
+    for t in (1e36, 1.1e37, 1e38, 3.4e38, np.inf):
+        for k, p, m in ((0, 1.0, 0.0), (40, 1.0, 0.0), (V // 2, 0.9, 0.0), (0, 0.5, 0.0), (0, 0.97, 0.2), (0, 1.0, 0.4)):
+            par = {"temperature": np.full(rows, t, np.float32), "top_k": np.full(rows, k, np.int32),
+                   "top_p": np.full(rows, p, np.float32), "min_p": np.full(rows, m, np.float32)}
+            check(z, par, rng.random(rows).astype(np.float32))
