@@ -377,10 +377,13 @@ __device__ __forceinline__ uint32_t chunk_max(const uint4& v) {
   return lo;
 }
 
-// 16 codes times 2^k.  fp16 holds every product that does not become 0 in e4m3, which rounds it once.
+// 16 codes times 2^k.  fp16 holds every product that does not become 0 in e4m3, which rounds it once.  A code that is
+// not 0 is 2^-9 or more and its product at most 448, so that k is below 18 where there is one; zeros alone may come
+// with any k (their new block goes by other values, or has none), and stay zeros with any finite factor.
 __device__ __forceinline__ uint4 chunk_scale(const uint4& v, int k) {
   uint32_t x[4] = {v.x, v.y, v.z, v.w};
-  const __half2 f = __float2half2_rn(kv8_pow2(min(max(k, -24), 15))), f2 = __float2half2_rn(kv8_pow2(max(k - 15, 0)));
+  const __half2 f = __float2half2_rn(kv8_pow2(min(max(k, -24), 15)));
+  const __half2 f2 = __float2half2_rn(kv8_pow2(min(max(k - 15, 0), 15)));
   auto two = [&](uint32_t c) -> uint32_t {
     const uint32_t u = f16x2_e4m3(c);
     __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&u), f);

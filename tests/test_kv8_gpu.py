@@ -703,3 +703,60 @@ def test_offsets_past_32_bits():
     c.attention(torch.zeros_like(x), out)  # the mean of the values
     got = (out * 131 - x).abs().max()
     assert float(got) <= 2.0 ** -3 * float(x.abs().max())  # the codes' rounding, 2^-4 of the value
+
+
+def zeros_cache(H, hd, P, lens, budget, k, v, ks, vs, w, table):
+    """A cache with the given numpy contents, and the blocks behind them for the kept slots; the oracle's copy."""
+    S, n0, out_cap = len(lens), k.shape[0], -(-budget // P)
+    grow = lambda a, x: np.concatenate([a, np.full((S * out_cap,) + a.shape[1:], x, a.dtype)])  # noqa: E731
+    ref = O.Cache(grow(k, 0x7F), grow(v, 0x7F), grow(ks, 1.0), grow(vs, 1.0), table, np.array(lens), grow(w, 0.0))
+    t = lambda a, d: torch.from_numpy(np.ascontiguousarray(a.astype(d))).cuda()  # noqa: E731
+    gpu = gb.KV8Cache(t(ref.k, np.uint8), t(ref.v, np.uint8), t(ref.ks, np.float32), t(ref.vs, np.float32),
+                      t(table, np.int32), t(ref.length, np.int32), t(ref.weight, np.float32),
+                      torch.zeros(1, dtype=torch.int32, device="cuda"))
+    return gpu, ref, np.arange(n0, n0 + S * out_cap, dtype=np.int32).reshape(S, out_cap)
+
+
+@pytest.mark.parametrize("kind", ["zero tokens of blocks with others", "zeros beside far smaller values", "NaN tokens and zeros",
+                                  "blocks outside the pool"])
+@pytest.mark.parametrize("H,hd,P", [(2, 64, 16), (1, 128, 64), (3, 32, 32), (1, 128, 128)])
+def test_evict_keeps_zeros(H, hd, P, kind):
+    """Kept codes that are zero stay zero (of either sign), however far apart their block's scale and the new block's are:
+    a block none of whose kept tokens is anything but zero has the smallest exponent."""
+    rng = np.random.default_rng(hd + P)
+    n = 2 * P
+    table = np.array([[1, 0]], np.int32)
+    k = rng.choice(np.array([0, 128], np.uint8), (2, H, P, hd))  # zeros of both signs
+    v = rng.choice(np.array([0, 128], np.uint8), (2, H, P, hd))
+    ks, vs = np.full((2, H), 2.0 ** -8), np.full((2, H), 2.0 ** 3)
+    heavy = rng.permutation(n - 1)[:P]  # the kept ones, beside the last
+    w = np.zeros((2, H, P))
+    for j in heavy:
+        w[table[0, j // P], :, j % P] = 1.0 + rng.random(H)
+    dropped = np.setdiff1d(np.arange(n - 1), heavy)
+    for j in dropped:  # what is not kept has values
+        for c in (k, v):
+            c[table[0, j // P], :, j % P] = rng.integers(0, 127, (H, hd))
+    if kind == "zeros beside far smaller values":
+        ks[1], vs[1] = 2.0 ** 20, 2.0 ** 40
+        ks[0], vs[0] = 2.0 ** -30, 2.0 ** -100
+        for j in range(P, n):
+            for c in (k, v):
+                c[0, :, j % P, ::3] = rng.integers(0, 127, c[0, :, j % P, ::3].shape)
+    if kind == "NaN tokens and zeros":
+        for j in heavy[::2]:
+            k[table[0, j // P], :, j % P] = 0x7F
+            v[table[0, j // P], :, j % P, 5] = 0xFF
+    if kind == "blocks outside the pool":
+        table = np.array([[-1, 2 + 5 * P]], np.int32)
+    gpu, ref, to = zeros_cache(H, hd, P, [n], P + 1, k, v, ks, vs, w, table)
+    kept = torch.zeros(1, H, P + 1, dtype=torch.int32, device="cuda")
+    gpu.evict(dev(to), P + 1, 1, kept)
+    assert np.array_equal(kept.cpu().numpy(), ref.evict(to, P + 1, 1))
+    assert np.array_equal(gpu.k_scale.cpu().numpy().astype(np.float64), ref.ks)
+    assert np.array_equal(gpu.v_scale.cpu().numpy().astype(np.float64), ref.vs)
+    for got, want in ((gpu.k, ref.k), (gpu.v, ref.v)):
+        got = got.cpu().numpy()
+        nan = (want & 127) == 127
+        assert np.array_equal((got & 127) == 127, nan) and np.array_equal(got[~nan], want[~nan])
+    assert int(gpu.flags) == (gb.FLAG_BLOCK_RANGE if kind == "blocks outside the pool" else 0)
