@@ -20,6 +20,8 @@
 // of four tokens; neither needs a transposition in memory.  P^T, the second
 // product's other operand, is S^T's registers with each 8 x 8 part transposed
 // (movmatrix).
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "kv8.cuh"
@@ -1271,9 +1273,9 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
       for (int i = 0; i < HD; i++) top = fmaxf(top, fabsf(to_f<T>(x[i])));
       int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
       e = min(max(e, -100), 100);
-      // a factor of the scores that is positive: the scale's sign goes with the row
+      // the scores' factor has no sign (a maximum may be taken before it): the scale's goes with the row
       const float up = copysignf(kv8_pow2(e), at.scale);
-      qf = fmaxf(kv8_pow2(-e) * fabsf(at.scale) * 1.4426950408889634f, 1e-36f);
+      qf = kv8_pow2(-e) * fabsf(at.scale) * 1.4426950408889634f;
 #pragma unroll
       for (int i = 0; i < HD; i += 8) {
         uint32_t f[4], lo[4];
@@ -1310,7 +1312,8 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         vl[g] = sh.vl[st][g];
-        f[g] = vl[g] == -INFINITY ? 1.f : qf * sh.ks[st][g];
+        // above 0: the scores that the row does not see are -infinity before the factor, and stay so
+        f[g] = vl[g] == -INFINITY ? 1.f : fmaxf(qf * sh.ks[st][g], FLT_MIN);
         all &= vl[g] != -INFINITY;
       }
       tmem_ld_wait();

@@ -760,3 +760,28 @@ def test_evict_keeps_zeros(H, hd, P, kind):
         nan = (want & 127) == 127
         assert np.array_equal((got & 127) == 127, nan) and np.array_equal(got[~nan], want[~nan])
     assert int(gpu.flags) == (gb.FLAG_BLOCK_RANGE if kind == "blocks outside the pool" else 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,news", [(64, 1, [1, 1, 1]), (64, 2, [6, 3, 1]), (64, 1, [30, 20, 3]), (64, 1, [100, 60, 2]),
+                                       (128, 1, [60, 1, 20]), (32, 3, [40, 40, 1])])
+@pytest.mark.parametrize("scale,gain", [(0.125, 2.0 ** -70), (0.125, 2.0 ** -30), (0.0, 1.0), (1e-38, 1.0)])
+def test_attention_factors_of_scores_that_underflow(hd, G, news, dtype, scale, gain):
+    """All-zero key blocks (the smallest scale) and tiny queries or scales: the scores are zero, and what a row does not
+    see stays unseen, in every form of the kernel."""
+    lens = [70, 9, 37]
+    gpu, ref, rng = make(23, [a + b for a, b in zip(lens, news)], 1, hd, 16)
+    for s in range(3):
+        for b in ref.table[s][s % 2::2]:
+            ref.k[b], ref.ks[b] = rng.choice(np.array([0, 128], np.uint8), ref.k[b].shape), 2.0 ** O.E_MIN
+    gpu.k.copy_(torch.from_numpy(ref.k))
+    gpu.k_scale.copy_(torch.from_numpy(ref.ks.astype(np.float32)))
+    ref.length[:] = lens
+    gpu.length.copy_(torch.tensor(lens, dtype=torch.int32))
+    st = starts(news)
+    q, q64 = rows_of(rng, int(st[-1]), G, hd, dtype, gain=gain)
+    out, lse, probs = check_attention(gpu, ref, q, q64, st, news, dtype, scale=scale)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    before = gpu.weight.clone()
+    gpu.accumulate(q, lse, start=dev(st), max_new=max(news), scale=scale)
+    assert abs(float((gpu.weight - before).double().sum()) - G * sum(news)) <= 1e-3 * G * sum(news)
