@@ -72,6 +72,10 @@ struct Exact {
   }
 };
 
+// A V block's factor of the weights, from its log2.  Past 2^120 (a block far above the one whose values set the running
+// maximum of scores + log2(V scale): all its weights have underflowed) it stays finite, so that they remain 0.
+__device__ __forceinline__ float v_factor(float log2) { return sfu_exp2(fminf(log2, 120.f)); }
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -530,8 +534,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
       for (int e = 0; e < 2; e++) {
         mm[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
         const float d = mm[e] - (mv[nt][e] == -INFINITY ? 0.f : mv[nt][e]);
-        c[0][e] = sfu_exp2(v0 + d);
-        c[1][e] = v0 == v1 ? c[0][e] : sfu_exp2(v1 + d);
+        c[0][e] = v_factor(v0 + d);
+        c[1][e] = v0 == v1 ? c[0][e] : v_factor(v1 + d);
       }
 #pragma unroll
       for (int gr = 0; gr < 2; gr++)
@@ -943,7 +947,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
     }
 #pragma unroll
     for (int kk = 0; kk < NG; kk++) {
-      const float c0 = sfu_exp2(vl[kk] + dv[0]), c1 = sfu_exp2(vl[kk] + dv[1]);
+      const float c0 = v_factor(vl[kk] + dv[0]), c1 = v_factor(vl[kk] + dv[1]);
       uint32_t p[4], plo[4];
 #pragma unroll
       for (int x = 0; x < 2; x++) {
@@ -1392,7 +1396,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
         uint32_t pk[16], pl[16];
 #pragma unroll
         for (int g = 0; g < 2; g++) {
-          const float c = sfu_exp2(vl[2 * half + g] + dv);
+          const float c = v_factor(vl[2 * half + g] + dv);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float e0 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i]), f[2 * half + g], -mm));

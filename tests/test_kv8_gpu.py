@@ -785,3 +785,24 @@ def test_attention_factors_of_scores_that_underflow(hd, G, news, dtype, scale, g
     before = gpu.weight.clone()
     gpu.accumulate(q, lse, start=dev(st), max_new=max(news), scale=scale)
     assert abs(float((gpu.weight - before).double().sum()) - G * sum(news)) <= 1e-3 * G * sum(news)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,n", [(64, 1, 1), (64, 2, 6), (64, 1, 30), (64, 1, 100), (128, 1, 60), (32, 3, 40)])
+def test_attention_value_scales_at_both_ends(hd, G, n, dtype):
+    """The whole weight on a block of zero values (the smallest scale), beside values of 2^27 and more: zeros, not
+    0 times infinity."""
+    gpu, ref, rng = make(24, [100 + n], 1, hd, 16)
+    gpu.length.fill_(100)
+    b0, st = int(ref.table[0, 0]), dev(starts([n]))
+    gpu.v[b0], gpu.v_scale[b0] = 0, 2.0 ** O.E_MIN
+    others = torch.from_numpy(ref.table[0, 1:].astype(np.int64)).cuda()
+    gpu.v_scale[others] = 2.0 ** 27
+    gpu.k.zero_()
+    gpu.k[b0, :, 3, 0] = 0x38  # 1.0 at slot 3
+    gpu.k_scale.fill_(1.0)
+    q = torch.zeros(n, G, hd, device="cuda", dtype=DT[dtype])
+    out, lse = torch.ones_like(q), torch.zeros(n, G, device="cuda")
+    q[:, :, 0] = 200.0
+    gpu.attention(q, out, start=st, max_new=n, lse=lse, scale=1.0)
+    assert (out == 0).all() and float((lse - 200.0).abs().max()) <= 200.0 * 2.0 ** -20
