@@ -82,6 +82,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
+// The power of two that brings a row's largest magnitude to 2^14 .. 2^15 (tiny rows: 2^100, so that it can be undone);
+// 0 where it is 0 or infinite.  At fp32's largest values it is 2^-113.
+__device__ __forceinline__ int row_exponent(float top) {
+  return top > 0.f && top < INFINITY ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 100) : 0;
+}
+
 // Rows of q as the B operand of the QK product, 8 NT of them.  bf16 rows are
 // exact in fp16 once a power of two has brought the row's largest magnitude to
 // 2^14 .. 2^15 (what falls below fp16's range then is under 2^-38 of it); fp32
@@ -134,8 +140,7 @@ struct QFrag {
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-      e = min(max(e, -100), 100);
+      const int e = row_exponent(top);
       const float up = kv8_pow2(e), down = kv8_pow2(-e) * scale * 1.4426950408889634f;
       f[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       f[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
@@ -834,8 +839,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-    e = min(max(e, -100), 100);
+    const int e = row_exponent(top);
     const float up = kv8_pow2(e);
     qf[half] = kv8_pow2(-e) * at.scale * 1.4426950408889634f;
 #pragma unroll
@@ -1275,8 +1279,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < HD; i++) top = fmaxf(top, fabsf(to_f<T>(x[i])));
-      int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-      e = min(max(e, -100), 100);
+      const int e = row_exponent(top);
       // the scores' factor has no sign (a maximum may be taken before it): the scale's goes with the row
       const float up = copysignf(kv8_pow2(e), at.scale);
       qf = kv8_pow2(-e) * fabsf(at.scale) * 1.4426950408889634f;
@@ -1532,8 +1535,7 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_many(Kv8Args a, At
 #pragma unroll
     for (int i = 0; i < DPT; i++) top = fmaxf(top, fabsf(to_f<T>(raw[i])));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    int e = top > 0.f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-    e = min(max(e, -100), 100);
+    const int e = row_exponent(top);
     const float up = kv8_pow2(e);
     uint8_t* to = smem + buf * TERMS * TILE;
 #pragma unroll

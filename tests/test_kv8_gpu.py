@@ -806,3 +806,24 @@ def test_attention_value_scales_at_both_ends(hd, G, n, dtype):
     q[:, :, 0] = 200.0
     gpu.attention(q, out, start=st, max_new=n, lse=lse, scale=1.0)
     assert (out == 0).all() and float((lse - 200.0).abs().max()) <= 200.0 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,n", [(64, 1, 1), (64, 2, 6), (64, 1, 30), (64, 1, 100), (128, 1, 60), (32, 3, 40)])
+def test_queries_at_the_end_of_the_range(hd, G, n, dtype):
+    """Queries as large as their type has: the slot with the largest score takes the whole weight."""
+    gpu, ref, rng = make(26, [100 + n], 1, hd, 16)
+    gpu.length.fill_(100)
+    b0, st = int(ref.table[0, 0]), dev(starts([n]))
+    gpu.k.zero_()
+    gpu.k[b0, :, 3, 0] = 0x38  # 1.0 at slot 3
+    gpu.k_scale.fill_(1.0)
+    want = torch.from_numpy(ref.values(0, 4, "v")[0][3, 0]).cuda().to(DT[dtype])
+    q = torch.zeros(n, G, hd, device="cuda", dtype=DT[dtype])
+    out, lse = torch.ones_like(q), torch.zeros(n, G, device="cuda")
+    for first in (2.0 ** 112, 2.0 ** 118, 2.0 ** 127):
+        q[:, :, 0] = first
+        q[:, :, 1] = -first / 2
+        gpu.attention(q, out, start=st, max_new=n, lse=lse, scale=0.25)
+        assert torch.equal(out, want.expand_as(out)), first
+        assert ((lse.double() - first / 4).abs() <= 2.0 ** -20 * first / 4).all()
