@@ -46,10 +46,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// the parts of (lo, hi) that pack_f16 rounded off, as fp16
-__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t p) {
+// the parts of (lo, hi) that pack_f16 rounded off, times `up`, as fp16
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t p, float up = 1.f) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-  return pack_f16(lo - f.x, hi - f.y);
+  return pack_f16((lo - f.x) * up, (hi - f.y) * up);
+}
+
+// Weights in fp16.  They come times 2^7: the largest is 2^15, and what falls below fp16's grid is under 2^-32 of the
+// largest weight.  With fp32 rows the second term comes times 2^11 more, against V times 2^-11 (exact: codes are
+// multiples of 2^-9, fp16's grid is 2^-24), and leaves under 2^-43: a long tail of small weights, the same for all,
+// keeps its sum.  (With neither factor 40,000 slots 12 nats below one lost 1.6e-4 of the output.)
+constexpr float P_LOG2 = 7.f, REST = 2048.f;
+__device__ __forceinline__ uint32_t pack_p_rest(float lo, float hi, uint32_t p) { return pack_rest(lo, hi, p, REST); }
+__device__ __forceinline__ uint32_t v_rest(uint32_t v) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1.f / REST));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
@@ -62,8 +73,8 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // The MMA cuts its sums off, which over hundreds of steps shows in fp32 (a long
-// context's outputs were off by 1e-5 of the largest).  fp32 rows let it add up
-// one step at a time and add the steps themselves, rounded to nearest.
+// context's outputs were off by 1e-5 of the largest).  For fp32 rows' scores it
+// adds up one step at a time, and the steps are added here, rounded to nearest.
 struct Exact {
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   __device__ __forceinline__ void add_to(float (&d)[4]) const {
@@ -71,10 +82,46 @@ struct Exact {
     for (int i = 0; i < 4; i++) d[i] += x[i];
   }
 };
+// Their outputs add up in the tensor cores over CHAIN slots; then they are added, rounded, to sums set aside, so that there are few roundings of either kind over a long context.
+constexpr int CHAIN = 256;
+// The warp MMA's sums set aside, four to an index, in the thread's local memory: they are touched once in a chain, and
+// registers and shared memory decide how many warps run.  (In shared memory, 16 KB more a block of 128 dimensions, two
+// blocks an SM in place of three: 6 sequences of 30,000 slots, 32 on 8 heads of 128, 117 us; so 82 us.)
+template <int N>
+struct Aside {
+  float4 mem[N > 0 ? N : 1];
+  float4* x;
+  bool any = false;
+  __device__ __forceinline__ Aside() {
+    x = mem;
+    if (N > 0) asm volatile("" : "+l"(x));  // (an address that the compiler does not see through: not registers)
+  }
+  __device__ __forceinline__ void take(int i, float (&o)[4]) {
+    float4 y = any ? x[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    y.x += o[0], y.y += o[1], y.z += o[2], y.w += o[3];
+    x[i] = y;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+  }
+  __device__ __forceinline__ void give(int i, float (&o)[4]) const {
+    const float4 y = x[i];
+    o[0] += y.x, o[1] += y.y, o[2] += y.z, o[3] += y.w;
+  }
+  __device__ __forceinline__ void scale(int i, float f0, float f1, float f2, float f3) {
+    float4 y = x[i];
+    y.x *= f0, y.y *= f1, y.z *= f2, y.w *= f3;
+    x[i] = y;
+  }
+};
+// Their sums of weights carry what an addition rounds off (Kahan): equal weights would round the same way each time.
+__device__ __forceinline__ void add_kept(float& sum, float& off, float x) {
+  const float y = x - off, t = sum + y;
+  off = (t - sum) - y;
+  sum = t;
+}
 
-// A V block's factor of the weights, from its log2.  Past 2^120 (a block far above the one whose values set the running
+// A V block's factor of the weights (2^P_LOG2 among it), from its log2.  Past 2^120 (a block far above the one whose values set the running
 // maximum of scores + log2(V scale): all its weights have underflowed) it stays finite, so that they remain 0.
-__device__ __forceinline__ float v_factor(float log2) { return sfu_exp2(fminf(log2, 120.f)); }
+__device__ __forceinline__ float v_factor(float log2) { return sfu_exp2(fminf(log2 + P_LOG2, 120.f)); }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
@@ -256,7 +303,7 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
       }
     // a row that sees nothing: zeros, and the log of an empty sum
     st.inv[r] = ll == 0.f ? 0.f : 1.f / ll;
-    st.back[r] = ll == 0.f ? 0.f : exp2f(mmv - mm);
+    st.back[r] = ll == 0.f ? 0.f : exp2f(mmv - mm - P_LOG2);
     if (split == 0 && at.lse) {
       const int rr = row0 + r;
       at.lse[(long)(r0 + rr / G) * heads + h * G + rr % G] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
@@ -319,7 +366,7 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
 // longer sequences finish last.
 template <typename T, int HD, int NT, int NW, int NS, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs at) {
-  constexpr int ROWS = 8 * NT;
+  constexpr int ROWS = 8 * NT, TERMS = sizeof(T) == 4 ? 2 : 1;
   constexpr int BPL = HD / 8;         // dimensions a lane loads of a V row
   constexpr int MT = HD / 16;         // 16-dimension tiles of the output
   constexpr int OP = HD + 4;          // pitch of a row of partial outputs
@@ -355,14 +402,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
     for (int nt = 0; nt < NT; nt++) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
   // of rows 8 nt + 2 t + e: running maximum of the scores (log2), that of scores + log2(V scale), the sum of
   // 2^(score - m), and the slots that the row sees
-  float m[NT][2], mv[NT][2], l[NT][2];
+  float m[NT][2], mv[NT][2], l[NT][2], l_off[NT][2];
   int see[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
       m[nt][e] = mv[nt][e] = -INFINITY;
-      l[nt][e] = 0.f;
+      l[nt][e] = l_off[nt][e] = 0.f;
       see[nt][e] = min(len + min(row0 + 8 * nt + 2 * t + e, R - 1) / G + 1, cap);
     }
 
@@ -370,6 +417,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   const int per = (tiles + n_split - 1) / n_split;
   const int t0 = min(tiles, split * per), t1 = min(tiles, t0 + per);
   Stage<HD>* ring = reinterpret_cast<Stage<HD>*>(smem) + w * NS;
+
+  // fp32 rows: the lane's outputs of the chains before
+  Aside<TERMS == 2 ? MT * NT : 0> aside;
+  int chained = 0;
 
   // block ids of the next tile to be requested, looked up one tile ahead and first touched when they are needed
   int b0 = -1, b1 = -1;
@@ -511,6 +562,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
         grow |= top[nt][e] > m[nt][e] + LAZY || topv[nt][e] > mv[nt][e] + LAZY;
       }
     if (__any_sync(0xffffffffu, grow)) {  // the lanes' maxima are brought together only where one of them says so
+      float fo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -522,14 +574,21 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
           }
           const float m1 = fmaxf(m[nt][e], top[nt][e]), mv1 = fmaxf(mv[nt][e], topv[nt][e]);
           const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[nt][e] - m1);
-          const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[nt][e] - mv1);
+          fo[nt][e] = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[nt][e] - mv1);
           m[nt][e] = m1, mv[nt][e] = mv1;
           l[nt][e] *= fl;
+          if (TERMS == 2) l_off[nt][e] *= fl;
 #pragma unroll
-          for (int i = 0; i < MT; i++) o[i][nt][e] *= fo, o[i][nt][2 + e] *= fo;
+          for (int i = 0; i < MT; i++) o[i][nt][e] *= fo[nt][e], o[i][nt][2 + e] *= fo[nt][e];
         }
+      if (TERMS == 2 && aside.any) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int i = 0; i < MT; i++) aside.scale(i * NT + nt, fo[nt][0], fo[nt][1], fo[nt][0], fo[nt][1]);
+      }
     }
-    // ---- weights: 2^(score - m) for the sum, times 2^(log2 V scale + m - mv) for the product with V's codes
+    // ---- weights: 2^(score - m) for the sum, times 2^(log2 V scale + m - mv + P_LOG2) for the product with V's codes
     uint32_t p[2][NT][2], plo[2][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
@@ -542,17 +601,22 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
         c[0][e] = v_factor(v0 + d);
         c[1][e] = v0 == v1 ? c[0][e] : v_factor(v1 + d);
       }
+      float lt[2] = {0.f, 0.f};  // fp32 rows: the tile's sums
 #pragma unroll
       for (int gr = 0; gr < 2; gr++)
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           const float x = sfu_exp2(sc[gr][nt][2 * half] - mm[0]), y = sfu_exp2(sc[gr][nt][2 * half + 1] - mm[1]);
-          l[nt][0] += x;
-          l[nt][1] += y;
+          (TERMS == 2 ? lt[0] : l[nt][0]) += x;
+          (TERMS == 2 ? lt[1] : l[nt][1]) += y;
           const uint32_t v = pack_f16(x * c[gr][0], y * c[gr][1]);
           p[gr][nt][half] = transpose8(v);
-          if (sizeof(T) == 4) plo[gr][nt][half] = transpose8(pack_rest(x * c[gr][0], y * c[gr][1], v));
+          if (TERMS == 2) plo[gr][nt][half] = transpose8(pack_p_rest(x * c[gr][0], y * c[gr][1], v));
         }
+      if (TERMS == 2) {
+        add_kept(l[nt][0], l_off[nt][0], lt[0]);
+        add_kept(l[nt][1], l_off[nt][1], lt[1]);
+      }
     }
     // ---- o += v^T p^T
     bool poison = false;
@@ -593,18 +657,16 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
             {f16x2_e4m3(x01), f16x2_e4m3(x01 >> 16), f16x2_e4m3(x23), f16x2_e4m3(x23 >> 16)},
             {f16x2_e4m3(y01), f16x2_e4m3(y01 >> 16), f16x2_e4m3(y23), f16x2_e4m3(y23 >> 16)}};
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < 2; i++) {
+          if (TERMS == 2) {  // the weights' second fp16 term
+            const uint32_t r0 = v_rest(aa[i][0]), r1 = v_rest(aa[i][1]), r2 = v_rest(aa[i][2]), r3 = v_rest(aa[i][3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            if (sizeof(T) == 2) {
-              mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
-            } else {  // fp32 outputs: the weights' second fp16 term too
-              Exact e;
-              mma(e.x, aa[i][0], aa[i][1], aa[i][2], aa[i][3], plo[gr][nt][0], plo[gr][nt][1]);
-              mma(e.x, aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
-              e.add_to(o[2 * c + i][nt]);
-            }
+            for (int nt = 0; nt < NT; nt++) mma(o[2 * c + i][nt], r0, r1, r2, r3, plo[gr][nt][0], plo[gr][nt][1]);
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+            mma(o[2 * c + i][nt], aa[i][0], aa[i][1], aa[i][2], aa[i][3], p[gr][nt][0], p[gr][nt][1]);
+        }
       }
     }
     if (__any_sync(0xffffffffu, poison)) {
@@ -622,6 +684,20 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
         }
       }
     }
+    if (TERMS == 2 && ++chained == CHAIN / TT) {
+#pragma unroll
+      for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) aside.take(i * NT + nt, o[i][nt]);
+      chained = 0;
+      aside.any = true;
+    }
+  }
+  if (TERMS == 2 && aside.any) {
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) aside.give(i * NT + nt, o[i][nt]);
   }
 
   // ---- join the warps: each row's maxima and sum, then the outputs at the common maximum
@@ -629,7 +705,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
-      float x = l[nt][e];
+      float x = TERMS == 2 ? l[nt][e] - l_off[nt][e] : l[nt][e];
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int r = 8 * nt + 2 * t + e;
@@ -861,7 +937,9 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
   float o[HD / 8][4];
 #pragma unroll
   for (int i = 0; i < HD / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, l_off[2] = {0.f, 0.f};
+  Aside<TERMS == 2 ? HD / 8 : 0> aside;  // fp32 rows: the thread's outputs of the chains before
+  int chained = 0;
 
   for (int tile = t0; tile < t1; tile++) {
     const int buf = (tile - t0) & 1;
@@ -927,6 +1005,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       grow |= top[half] > m[half] + LAZY || topv[half] > mv[half] + LAZY;
     }
     if (__any_sync(0xffffffffu, grow)) {  // the lanes' maxima are brought together only where one of them says so
+      float fo[2];
 #pragma unroll
       for (int half = 0; half < 2; half++) {
 #pragma unroll
@@ -936,14 +1015,19 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
         }
         const float m1 = fmaxf(m[half], top[half]), mv1 = fmaxf(mv[half], topv[half]);
         const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m[half] - m1);
-        const float fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[half] - mv1);
+        fo[half] = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[half] - mv1);
         m[half] = m1, mv[half] = mv1;
         l[half] *= fl;
+        if (TERMS == 2) l_off[half] *= fl;
 #pragma unroll
-        for (int i = 0; i < HD / 8; i++) o[i][2 * half] *= fo, o[i][2 * half + 1] *= fo;
+        for (int i = 0; i < HD / 8; i++) o[i][2 * half] *= fo[half], o[i][2 * half + 1] *= fo[half];
+      }
+      if (TERMS == 2 && aside.any) {
+#pragma unroll
+        for (int i = 0; i < HD / 8; i++) aside.scale(i, fo[0], fo[0], fo[1], fo[1]);
       }
     }
-    float mm[2], dv[2];
+    float mm[2], dv[2], lt[2] = {0.f, 0.f};  // fp32 rows: the tile's sums
 #pragma unroll
     for (int half = 0; half < 2; half++) {
       mm[half] = m[half] == -INFINITY ? 0.f : m[half];
@@ -957,32 +1041,30 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       for (int x = 0; x < 2; x++) {
         const float e0 = sfu_exp2(sc[2 * kk + x][0] - mm[0]), e1 = sfu_exp2(sc[2 * kk + x][1] - mm[0]);
         const float e2 = sfu_exp2(sc[2 * kk + x][2] - mm[1]), e3 = sfu_exp2(sc[2 * kk + x][3] - mm[1]);
-        l[0] += e0 + e1;
-        l[1] += e2 + e3;
+        (TERMS == 2 ? lt[0] : l[0]) += e0 + e1;
+        (TERMS == 2 ? lt[1] : l[1]) += e2 + e3;
         p[2 * x] = pack_f16(e0 * c0, e1 * c0);
         p[2 * x + 1] = pack_f16(e2 * c1, e3 * c1);
         if (TERMS == 2) {
-          plo[2 * x] = pack_rest(e0 * c0, e1 * c0, p[2 * x]);
-          plo[2 * x + 1] = pack_rest(e2 * c1, e3 * c1, p[2 * x + 1]);
+          plo[2 * x] = pack_p_rest(e0 * c0, e1 * c0, p[2 * x]);
+          plo[2 * x + 1] = pack_p_rest(e2 * c1, e3 * c1, p[2 * x + 1]);
         }
       }
 #pragma unroll
       for (int i = 0; i < HD / 8; i += 2) {
         uint32_t b[4];
         ldsm4t(b, vb + v_off[i / 2] + kk * 32 * HD);
-        if (TERMS == 1) {
-          mma(o[i], p[0], p[1], p[2], p[3], b[0], b[1]);
-          mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
-        } else {
-          Exact e0, e1;
-          mma(e0.x, plo[0], plo[1], plo[2], plo[3], b[0], b[1]);
-          mma(e1.x, plo[0], plo[1], plo[2], plo[3], b[2], b[3]);
-          mma(e0.x, p[0], p[1], p[2], p[3], b[0], b[1]);
-          mma(e1.x, p[0], p[1], p[2], p[3], b[2], b[3]);
-          e0.add_to(o[i]);
-          e1.add_to(o[i + 1]);
+        if (TERMS == 2) {
+          mma(o[i], plo[0], plo[1], plo[2], plo[3], v_rest(b[0]), v_rest(b[1]));
+          mma(o[i + 1], plo[0], plo[1], plo[2], plo[3], v_rest(b[2]), v_rest(b[3]));
         }
+        mma(o[i], p[0], p[1], p[2], p[3], b[0], b[1]);
+        mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
       }
+    }
+    if (TERMS == 2) {
+      add_kept(l[0], l_off[0], lt[0]);
+      add_kept(l[1], l_off[1], lt[1]);
     }
     if (poison) {  // the NaN that were taken out go into the rows that see them
       for (int row = 0; row < MT; row++) {
@@ -998,10 +1080,21 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
             if ((c[8 * i + 2 * t + (y & 1)] & 0x7f) == 0x7f && j < see[y >> 1]) o[i][y] = __int_as_float(0x7fc00000);
       }
     }
+    if (TERMS == 2 && ++chained == CHAIN / MT) {
+#pragma unroll
+      for (int i = 0; i < HD / 8; i++) aside.take(i, o[i]);
+      chained = 0;
+      aside.any = true;
+    }
+  }
+  if (TERMS == 2 && aside.any) {
+#pragma unroll
+    for (int i = 0; i < HD / 8; i++) aside.give(i, o[i]);
   }
 
 #pragma unroll
   for (int half = 0; half < 2; half++) {
+    if (TERMS == 2) l[half] -= l_off[half];
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
   }
@@ -1021,7 +1114,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // ---------------------------------------------------------------- many rows: tcgen05
 //
 // 128 rows of one key / value head and sequence over one of the cluster's equal
-// parts of the slots, 64 slots a tile.  Two warps turn codes into fp16 tiles
+// parts of the slots, 64 slots a tile.  Two or four warps turn codes into fp16 tiles
 // (128-byte swizzle, as a TMA load would leave them) through a ring of stages;
 // one thread issues S = Q K^T into one of two TMEM buffers and, a tile later,
 // O += P V with P read from TMEM; four warps, a row a thread, do the softmax:
@@ -1029,9 +1122,10 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // fp16 over its scores, and O is rescaled in TMEM only where a running maximum
 // has to grow.  Statistics and joins are those of k_kv8_attn.
 //
-// fp32 rows: Q and P are two fp16 terms each, and the products of four tiles at a
-// time are added to sums of their own (FLUSH): 6e-7 of the outputs' norm over
-// 20,000 slots, where sums left in the tensor core drift off by 2.7e-6.
+// fp32 rows: Q and P are two fp16 terms each (a stage has V twice, for P's second
+// term times 2^-11), and the products of four tiles at a time are added to sums
+// of their own (FLUSH): 6e-7 of the outputs' norm over 20,000 and 100,000 slots,
+// where sums left in the tensor core drift off by 2.7e-6.
 //
 // B200: 2 sequences of 900 to 1000 new rows over 3000 to 4000 slots, 16 heads of
 // 64: 100 us, 310 TFLOP/s of the visible products (the warp MMA's blocks of 64
@@ -1040,10 +1134,9 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // five other instructions each.  63 to 200 new rows over up to 1501 slots, 4
 // sequences of 25 heads: 28 us (33 us), two fifths of it before the first tile
 // and in the join.  fp32, 3 sequences of 71 new rows over 4300 slots, 8 heads of
-// 128: 67 us (the warp MMA's blocks: 100 us).
+// 128: 68 us (with two converting warps 81 us, the warp MMA's blocks 100 us).
 constexpr int CR = 128, CT = 64;             // rows of a block, slots of a tile
-constexpr int C_SOFT = 4, C_MAKE = 2;        // softmax and converting warps; one more issues
-constexpr int C_THREADS = (C_SOFT + 1 + C_MAKE) * 32;
+constexpr int C_SOFT = 4;                    // softmax warps; one more issues, others convert
 
 template <typename T, int HD>
 struct TcShape {
@@ -1051,12 +1144,15 @@ struct TcShape {
   static constexpr int MINB = TERMS == 2 && HD == 128 ? 1 : 2;          // blocks an SM
   // fp32 rows: the products add up over FLUSH tiles only; then they are added, rounded to nearest, to the sums so far,
   // which have their own columns (the tensor core cuts its sums off: over hundreds of tiles that shows in fp32)
-  static constexpr int FLUSH = TERMS == 2 ? 4 : 1 << 30, SUMS = 128 + (HD == 128 ? 128 : 64);
+  static constexpr int FLUSH = TERMS == 2 ? CHAIN / CT : 1 << 30, SUMS = 128 + (HD == 128 ? 128 : 64);
   static constexpr int COLS = TERMS == 2 && HD == 128 ? 512 : 256;      // TMEM columns
+  static constexpr int MAKE = MINB == 1 ? 4 : 2;                        // converting warps (two blocks of an SM: two each)
+  static constexpr int THREADS = (C_SOFT + 1 + MAKE) * 32;
   static constexpr int NB = HD == 128 ? 2 : 1, WD = HD < 64 ? HD : 64;  // blocks of 64 dimensions, dimensions a block
-  static constexpr int NS = HD == 128 ? 2 : 3;                          // stages
+  static constexpr int NS = HD == 128 || TERMS == 2 ? 2 : 3;            // stages
   static constexpr int QB = CR * 128, TB = CT * 128;                    // bytes of a block's Q, and of K or V
-  static constexpr int KV = TERMS * NB * QB, STAGE = 2 * NB * TB;       // the first stage; K blocks, then V blocks
+  // the first stage: K blocks, V blocks, fp32 rows: V blocks for the weights' second term
+  static constexpr int KV = TERMS * NB * QB, STAGE = (1 + TERMS) * NB * TB;
   static constexpr int END = KV + NS * STAGE, PITCH = HD + 4;           // (later: outputs [CR][PITCH])
   static_assert(CR * PITCH * 4 <= END, "the outputs take the tiles' place");
 };
@@ -1064,16 +1160,16 @@ struct TcShared {
   RowStats<CR> stats;
   uint64_t q_full, kv_full[3], kv_empty[3], s_full[2], p_full[2], pv_done[2];
   float ks[3][4], vl[3][4];  // a stage's groups: K scale, log2 of the V scale (-infinity: no block)
-  int nan[3][C_MAKE];        // a NaN has been taken out of the stage's V
+  int nan[3][4];             // a NaN has been taken out of the stage's V
   uint32_t tmem, no_flags;
   int abort;
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
+__global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MINB)) k_kv8_attn_tc(Kv8Args a, AttnArgs at) {
   using S = TcShape<T, HD>;
   using namespace sm100;
-  constexpr int CPR = HD / 16, CPT = (CT * CPR + C_MAKE * 32 - 1) / (C_MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
+  constexpr int CPR = HD / 16, CPT = (CT * CPR + S::MAKE * 32 - 1) / (S::MAKE * 32);  // 16-code chunks a row; of K, and of V, a thread
   extern __shared__ uint8_t raw_smem[];
   // swizzled tiles need 1024-byte alignment
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
@@ -1100,7 +1196,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
   if (tid == 0) {
     mbar_init(q_full, C_SOFT);
     for (int i = 0; i < 3; i++) {
-      mbar_init(kv_full0 + 8 * i, C_MAKE);
+      mbar_init(kv_full0 + 8 * i, S::MAKE);
       mbar_init(kv_empty0 + 8 * i, 1);
     }
     for (int u = 0; u < 2; u++) {
@@ -1125,7 +1221,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
     // ================= codes to fp16 tiles
     const int me = tid - (C_SOFT + 1) * 32, w = warp - C_SOFT - 1;
     const int trow = me / CPR, part = me % CPR;
-    constexpr int STEP = C_MAKE * 32 / CPR;  // rows between a thread's chunks
+    constexpr int STEP = S::MAKE * 32 / CPR;  // rows between a thread's chunks
     // the next tile's codes in flight, and the block ids of the tile behind it
     int blk[CPT], gblk = -1;
     uint4 ck[CPT], cv[CPT];
@@ -1187,8 +1283,11 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
           const uint32_t off = (part / 4) * S::TB + half_at<64>(row, part % 4 * 2 + i);
           *reinterpret_cast<uint4*>(tk + off) =
               make_uint4(f16x2_e4m3(x[2 * i]), f16x2_e4m3(x[2 * i] >> 16), f16x2_e4m3(x[2 * i + 1]), f16x2_e4m3(x[2 * i + 1] >> 16));
-          *reinterpret_cast<uint4*>(tv + off) =
+          const uint4 v =
               make_uint4(f16x2_e4m3(y[2 * i]), f16x2_e4m3(y[2 * i] >> 16), f16x2_e4m3(y[2 * i + 1]), f16x2_e4m3(y[2 * i + 1] >> 16));
+          *reinterpret_cast<uint4*>(tv + off) = v;
+          if (S::TERMS == 2)
+            *reinterpret_cast<uint4*>(tv + S::NB * S::TB + off) = make_uint4(v_rest(v.x), v_rest(v.y), v_rest(v.z), v_rest(v.w));
         }
       }
       if (me < 4) {
@@ -1228,7 +1327,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
           for (int x = S::TERMS - 1; x >= 0; x--)
 #pragma unroll
             for (int kk = 0; kk < CT / 16; kk++)
-              mma_bf16_ts(tmem + 128 + 64 * nb, tmem + 64 * u + 32 * x + 8 * kk, desc_sw128(v + nb * S::TB + kk * 2048, S::TB, 1024),
+              mma_bf16_ts(tmem + 128 + 64 * nb, tmem + 64 * u + 32 * x + 8 * kk, desc_sw128(v + (x * S::NB + nb) * S::TB + kk * 2048, S::TB, 1024),
                           id_o, ((S::TERMS == 2 ? i % S::FLUSH : i) > 0 || kk > 0 || x < S::TERMS - 1) ? 1u : 0u);
         mma_commit(pv_done0 + 8 * u);
         mma_commit(kv_empty0 + 8 * (i % S::NS));
@@ -1301,7 +1400,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
       if (lane == 0) mbar_arrive(q_full);
     }
     const int see = min(len + min(rr, R - 1) / G + 1, cap);
-    float m = -INFINITY, mv = -INFINITY, l = 0.f;
+    float m = -INFINITY, mv = -INFINITY, l = 0.f, l_off = 0.f;
     uint32_t nan_dims[HD / 32];
 #pragma unroll
     for (int i = 0; i < HD / 32; i++) nan_dims[i] = 0;
@@ -1348,6 +1447,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
         const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m - m1), fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv - mv1);
         m = m1, mv = mv1;
         l *= fl;
+        if (S::TERMS == 2) l_off *= fl;
         if (j > 0) {
           // O holds the products of the tiles before.  S of this tile was issued after P V of tile j - 2, so that of
           // tile j - 1 is the only one that may be in flight.
@@ -1393,6 +1493,7 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
         }
         tmem_st_wait();
       }
+      float lt = 0.f;  // fp32 rows: the tile's sum
       const float mm = m == -INFINITY ? 0.f : m, dv = mm - (mv == -INFINITY ? 0.f : mv);
 #pragma unroll
       for (int half = 0; half < 2; half++) {
@@ -1404,17 +1505,21 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
           for (int i = 0; i < 16; i += 2) {
             const float e0 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i]), f[2 * half + g], -mm));
             const float e1 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i + 1]), f[2 * half + g], -mm));
-            l += e0 + e1;
+            (S::TERMS == 2 ? lt : l) += e0 + e1;
             pk[8 * g + i / 2] = pack_f16(e0 * c, e1 * c);
-            if (S::TERMS == 2) pl[8 * g + i / 2] = pack_rest(e0 * c, e1 * c, pk[8 * g + i / 2]);
+            if (S::TERMS == 2) pl[8 * g + i / 2] = pack_p_rest(e0 * c, e1 * c, pk[8 * g + i / 2]);
           }
         }
         // over the scores, which have been read: the A operand of P V (fp32 rows: its second terms behind it)
         tmem_st_32x32b_x16(trow + 64 * u + 16 * half, pk);
         if (S::TERMS == 2) tmem_st_32x32b_x16(trow + 64 * u + 32 + 16 * half, pl);
       }
+      if (S::TERMS == 2) add_kept(l, l_off, lt);
       tmem_st_wait();
-      if (sh.nan[st][0] | sh.nan[st][1]) {
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < S::MAKE; i++) nan |= sh.nan[st][i] != 0;
+      if (nan) {
         for (int i = 0; i < CT && base + i < see; i++) {
           const int b = ids[(base + i) >> a.lgP];
           if ((unsigned)b >= (unsigned)a.n_blocks) continue;
@@ -1457,13 +1562,13 @@ __global__ void __launch_bounds__(C_THREADS, (TcShape<T, HD>::MINB)) k_kv8_attn_
 #pragma unroll
       for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     }
-    sh.stats.m[r] = m, sh.stats.mv[r] = mv, sh.stats.l[r] = l;
+    sh.stats.m[r] = m, sh.stats.mv[r] = mv, sh.stats.l[r] = S::TERMS == 2 ? l - l_off : l;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == C_SOFT) tmem_dealloc(tmem, S::COLS);
-  join_blocks<T, HD, CR, S::PITCH, C_THREADS>(sh.stats, reinterpret_cast<float*>(smem), n_split, split, min(CR, R - row0), at,
+  join_blocks<T, HD, CR, S::PITCH, (TcShape<T, HD>::THREADS)>(sh.stats, reinterpret_cast<float*>(smem), n_split, split, min(CR, R - row0), at,
                                                  r0, row0, h, a.H * G);
 }
 
@@ -1850,7 +1955,7 @@ bool launch_attn_tc(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len) {
     const double waves = blocks * i / places, cost = (waves <= 1.0 ? 1.0 : waves + 0.4) * (tiles / i + 6.0);
     if (i == 1 || cost < best) best = cost, split = i;
   }
-  return launch_split<k_kv8_attn_tc<T, HD>>(c, a, at, split, row_tiles, C_THREADS, 1024 + TcShape<T, HD>::END + sizeof(TcShared));
+  return launch_split<k_kv8_attn_tc<T, HD>>(c, a, at, split, row_tiles, (TcShape<T, HD>::THREADS), 1024 + TcShape<T, HD>::END + sizeof(TcShared));
 }
 
 template <typename T, int HD>

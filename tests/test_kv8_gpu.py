@@ -827,3 +827,40 @@ def test_queries_at_the_end_of_the_range(hd, G, n, dtype):
         gpu.attention(q, out, start=st, max_new=n, lse=lse, scale=0.25)
         assert torch.equal(out, want.expand_as(out)), first
         assert ((lse.double() - first / 4).abs() <= 2.0 ** -20 * first / 4).all()
+
+
+@pytest.mark.parametrize("max_len", [0, 1])
+@pytest.mark.parametrize("z", [6.0, 12.0, 18.0])
+@pytest.mark.parametrize("hd,P,G,n", [(64, 16, 1, 1), (64, 128, 3, 5), (128, 64, 4, 1), (128, 16, 4, 3), (32, 16, 2, 1),
+                                      (64, 16, 1, 40), (64, 64, 3, 21), (32, 32, 2, 20), (64, 16, 1, 100), (32, 16, 1, 70),
+                                      (128, 32, 1, 30), (128, 16, 5, 27)])
+def test_a_heavy_slot_over_a_long_flat_tail_in_fp32(hd, P, G, n, z, max_len):
+    """One slot z nats above 40,000 equal ones, whose weights, though small each, are together a part of the output: a
+    rounding that depends on the largest weight would show with its full sum, since it is the same for all of them.
+
+    |o - o64| <= (2 B + 4) 2^-21 V as in the other fp32 cases, with B = z sum |q k| = z: of a weight relative to itself,
+    beside the sums: 32 steps in the tensor core, cut off at 2^-23 of their sum or less, and one addition, 2^-24, for every
+    256 slots that one block (here all: max_len 1) has, of up to V each."""
+    tail = 40000
+    blocks = -(-(tail + 1 + n) // P)
+    c = gb.KV8Cache.allocate(1, 1, hd, P, blocks)
+    c.length.fill_(tail)
+    vt = torch.from_numpy(O.encode(np.linspace(-1.0, 1.0, hd))).cuda()  # the tail's values and the heavy slot's: fixed codes
+    vh = torch.flip(vt, (0,))
+    c.v.copy_(vt.expand_as(c.v))
+    c.v[0, :, 0] = vh
+    c.k[0, 0, 0, 0] = 0x38  # 1.0 where the others have 0
+    c.k_scale.fill_(1.0), c.v_scale.fill_(1.0)
+    q = torch.zeros(n, G, hd, device="cuda")
+    q[:, :, 0] = z + torch.linspace(0, 0.3, n * G, device="cuda").reshape(n, G)
+    out, lse = torch.zeros_like(q), torch.zeros(n, G, device="cuda")
+    c.attention(q, out, start=dev(starts([n])), max_new=n, lse=lse, scale=1.0, max_len=max_len)
+    z64 = q[:, :, 0].double()
+    e = torch.exp(-z64) * (tail + torch.arange(n, device="cuda", dtype=torch.float64))[:, None]  # the visible tail
+    h64, t64 = (torch.from_numpy(O.decode(x.cpu().numpy())).cuda() for x in (vh, vt))
+    want = (h64 + e[..., None] * t64) / (1 + e[..., None])
+    B = z + 0.3
+    tol = (2 * B + 4) * 2.0 ** -21 + 32 * 2.0 ** -23 + (tail // 256) * 2.0 ** -24
+    err = float((out.double() - want).abs().max())
+    assert err <= tol, (err, tol)
+    assert float((lse.double() - (z64 + torch.log1p(e))).abs().max()) <= B * 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -23 * (B + 11)
