@@ -145,7 +145,7 @@ struct gpt_model {
   uint8_t *dyb, *dqkv, *datt, *dh;
   int32_t *stok, *spos, *nuniq;
   double* norm_part;
-  float* scal;  // [0] micro loss, [1] step loss, [2] grad norm, [3] flags (uint32)
+  float* scal;  // [0] micro loss, [1] step loss, [2] grad norm, [3] flags (uint32), [4] a gpt_generate_kv8 call's flags
   int32_t* argmax_out;
   size_t splitk_floats = 0;
   int part_blocks = 0;
@@ -209,6 +209,7 @@ struct gpt_model {
   bool have_forward = false;
   bool ce_grad_done = false;
   int64_t drop_counter = 0;
+  uint32_t* kv8_flags() const { return reinterpret_cast<uint32_t*>(scal + 4); }
   uint32_t reported = 0;
   std::string err;
 
@@ -530,7 +531,6 @@ gpt_status sync_and_flags(gpt_model* m, const char* where, float* h_scal /* 4 fl
   uint32_t fresh = fl & ~m->reported;
   m->reported |= fl;
   if (fresh & FLAG_TIMEOUT) return fail(m, GPT_ERR_TIMEOUT, "%s: a bounded device wait ran out", where);
-  if (fresh & FLAG_PROMPT_LEN) return fail(m, GPT_ERR_INVALID_ARG, "%s: a prompt's length is outside [1, T0]", where);
   if (fresh & FLAG_TOKEN) return fail(m, GPT_ERR_TOKEN_RANGE, "%s: token id outside [0, vocab_size)", where);
   if (fresh & (FLAG_LOSS | FLAG_NORM)) return fail(m, GPT_ERR_NONFINITE, "%s: non-finite loss or gradient norm", where);
   return GPT_OK;
@@ -1194,14 +1194,16 @@ static gpt_status generate_kv8_body(gpt_model* m, const Kv8Args& cache, const in
   const float saved_drop = m->cfg.dropout;
   m->cfg.dropout = 0.f;  // inference runs without dropout
   cudaMemsetAsync(m->stage_tgt, 0, (size_t)m->M * 4, c.stream);
+  cudaMemsetAsync(m->kv8_flags(), 0, 4, c.stream);
   // prefill: the padded prompts through the full forward, their lengths in the embedding sort's scratch
-  prompt_rows(c, d_prompt, d_prompt_len, B, T0, Tn, m->stage_idx, m->spos);
+  prompt_rows(c, d_prompt, d_prompt_len, B, T0, Tn, m->stage_idx, m->spos, m->kv8_flags());
   check_tokens(c, m->stage_idx, m->stage_tgt, m->M, m->V, m->idx, m->tgt);
   gpt_status s = forward_any(m, false, m->scal + 6, 1.0f / (float)m->M, 0);
   m->cfg.dropout = saved_drop;
   if (s != GPT_OK) return s;
   Kv8Gen kv;
   kv.cache = cache;
+  kv.cache.flags = m->kv8_flags();  // the call's own: it reports them whether or not the cache has a word
   kv.len = m->spos;
   kv.weights = budget > 0;
   kv.bound = T0;
@@ -1248,6 +1250,7 @@ static gpt_status generate_kv8_body(gpt_model* m, const Kv8Args& cache, const in
     a.max_new = 1;
     kv8_advance(c, a, capacity);
   }
+  add_flags(c, m->kv8_flags(), cache.flags);
   return check_cuda(m, "generate_kv8");
 }
 
@@ -1891,12 +1894,22 @@ gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int3
                            (uint64_t)(uintptr_t)d_out, (uint64_t)(uintptr_t)d_logp};
   static_assert(16 * 8 + sizeof(gpt_kv8_cache) <= sizeof key, "the key holds the cache");
   memcpy(&key[16], cache, sizeof *cache);
-  return run_generation(m, key, "generate_kv8", [&] {
+  s = run_generation(m, key, "generate_kv8", [&] {
     return m->bf16m ? generate_kv8_body<bf16>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
                                               d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp)
                     : generate_kv8_body<float>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
                                                d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp);
   });
+  if (s == GPT_ERR_CUDA) return s;
+  uint32_t fl = 0;  // this call's, reported at every call
+  cudaMemcpyAsync(&fl, m->kv8_flags(), 4, cudaMemcpyDeviceToHost, m->ctx.stream);
+  if (cudaStreamSynchronize(m->ctx.stream) != cudaSuccess) return check_cuda(m, "generate_kv8");
+  m->reported |= fl;
+  if (fl & FLAG_TIMEOUT) return fail(m, GPT_ERR_TIMEOUT, "generate_kv8: a bounded device wait ran out");
+  if (fl & FLAG_PROMPT_LEN) return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: a prompt's length is outside [1, T0]");
+  if (fl & FLAG_BLOCK) return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: a table names a block outside [0, n_blocks)");
+  if (fl) return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: the cache's tables do not hold the tokens (flags 0x%x)", fl);
+  return s;
 }
 
 gpt_status gpt_eval_loss(gpt_model* m, const void* d_stream, uint64_t stream_len, uint64_t data_seed,

@@ -188,6 +188,13 @@ __global__ void k_prompt_rows(const int32_t* __restrict__ prompt, const int32_t*
   if (threadIdx.x == 0) len_out[b] = n;
 }
 
+// A call's flags into the model's word and, but for the prompts' length, the cache's.
+__global__ void k_add_flags(const uint32_t* __restrict__ from, uint32_t* model, uint32_t* cache) {
+  const uint32_t f = *from;
+  if (f) atomicOr(model, f);
+  if (cache && (f & ~FLAG_PROMPT_LEN)) atomicOr(cache, f & ~FLAG_PROMPT_LEN);
+}
+
 // Row len[b] - 1 of each sequence's T rows.
 template <typename V>
 __global__ void k_last_rows(const V* __restrict__ x, const int32_t* __restrict__ len, int T, long row, V* __restrict__ out) {
@@ -213,9 +220,14 @@ __global__ void k_embed_rows(const int32_t* __restrict__ tok, const int32_t* __r
 
 }  // namespace
 
-void prompt_rows(Ctx& c, const int32_t* prompt, const int32_t* len, int B, int T0, int T, int32_t* ids, int32_t* len_out) {
+void prompt_rows(Ctx& c, const int32_t* prompt, const int32_t* len, int B, int T0, int T, int32_t* ids, int32_t* len_out,
+                 uint32_t* flags) {
   LaunchScope s(c, "prompt_rows");
-  k_prompt_rows<<<B, 256, 0, c.stream>>>(prompt, len, T0, T, ids, len_out, c.flags);
+  k_prompt_rows<<<B, 256, 0, c.stream>>>(prompt, len, T0, T, ids, len_out, flags);
+}
+void add_flags(Ctx& c, const uint32_t* from, uint32_t* cache_flags) {
+  LaunchScope s(c, "add_flags");
+  k_add_flags<<<1, 1, 0, c.stream>>>(from, c.flags, cache_flags);
 }
 void last_rows(Ctx& c, const void* x, const int32_t* len, int B, int T, long row_bytes, void* out) {
   LaunchScope s(c, "last_rows");

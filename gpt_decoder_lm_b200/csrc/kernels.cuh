@@ -290,9 +290,12 @@ bool sample_rows_each(Ctx& c, const void* logits, bool bf16_logits, int rows, in
                       const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, int32_t* out,
                       float* logp);
 
-// generation from prompts of different lengths: the padded ids [B, T] and the checked lengths; each sequence's last
-// prompt row of an activation; the embedding of one token a sequence at position len[b] + add
-void prompt_rows(Ctx& c, const int32_t* prompt, const int32_t* len, int B, int T0, int T, int32_t* ids, int32_t* len_out);
+// generation from prompts of different lengths: the padded ids [B, T] and the checked lengths (bad ones in flags); each
+// sequence's last prompt row of an activation; the embedding of one token a sequence at position len[b] + add; the
+// call's flags added to the model's and the cache's (nullable)
+void prompt_rows(Ctx& c, const int32_t* prompt, const int32_t* len, int B, int T0, int T, int32_t* ids, int32_t* len_out,
+                 uint32_t* flags);
+void add_flags(Ctx& c, const uint32_t* from, uint32_t* cache_flags);
 void last_rows(Ctx& c, const void* x, const int32_t* len, int B, int T, long row_bytes, void* out);
 void embed_rows(Ctx& c, const int32_t* tok, const int32_t* len, int add, int T, int V, const float* wte, const float* wpe,
                 float* res, int B, int d);

@@ -80,7 +80,7 @@ enum {
   GPT_FLAG_NONFINITE_LOSS = 1u << 1,
   GPT_FLAG_NONFINITE_NORM = 1u << 2,
   GPT_FLAG_TIMEOUT = 1u << 3,
-  /* gpt_kv8_* (the cache's own flag word, gpt_kv8_cache.d_flags) */
+  /* gpt_kv8_* (the cache's own flag word, gpt_kv8_cache.d_flags; gpt_generate_kv8: the model's too) */
   GPT_FLAG_BLOCK_RANGE = 1u << 4, /* a table entry was outside [0, n_blocks): its tokens were left out */
   GPT_FLAG_CACHE_FULL = 1u << 5,  /* tokens past the table's capacity were not stored                  */
   GPT_FLAG_ROW_RANGE = 1u << 6,   /* offsets were out of order or out of range: a sequence was left out */
@@ -536,8 +536,12 @@ gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, i
  * Draws as gpt_sample_rows with d_temperature .. d_min_p [batch_size] (each
  * nullable) and d_uniform fp32 [n_new, batch_size].  d_out int32 [batch_size,
  * n_new] receives the new tokens, d_logp (nullable, fp32, the same shape) their
- * log-probabilities.  The last token drawn is not appended.  Otherwise as
- * gpt_generate: overwrites the activations, synchronising, replayed as a CUDA
+ * log-probabilities.  The last token drawn is not appended.  What only the
+ * device sees is returned, at every such call: a prompt's length outside
+ * [1, T0] or a block id outside the pool, in either table, where the call came
+ * to use it, as GPT_ERR_INVALID_ARG, a bounded wait that ran out as
+ * GPT_ERR_TIMEOUT (the outputs are not valid then); the bits are set in
+ * cache->d_flags too, where there is one.  Otherwise as gpt_generate: overwrites the activations, synchronising, replayed as a CUDA
  * graph when a call repeats; GPT_ERR_UNSUPPORTED with recompute, or for a
  * head_dim that the cache does not have. */
 gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int32_t* d_prompt,

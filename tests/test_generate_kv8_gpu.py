@@ -208,3 +208,44 @@ def test_recompute_is_refused():
                        torch.zeros(4, 2, dtype=torch.int32, device="cuda"))
     assert e.value.name == "GPT_ERR_UNSUPPORTED"
     m.close()
+
+
+@pytest.mark.parametrize("flags", [True, False])
+def test_tables_outside_the_pool_are_reported(flags):
+    """A block id outside the pool, in either table: the call returns an error, each time, whether or not the cache has a
+    flag word of its own; a good call after it is good."""
+    m, _, oc = setup("char", "bf16")
+    B = oc.batch_size
+    cache, other = make_cache(oc, 16, 2)
+    if not flags:
+        cache = gb.KV8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.table, cache.length, cache.weight)
+    n_new = 40
+    prompt, U = torch.zeros(B, 8, dtype=torch.int32, device="cuda"), torch.full((n_new, B), 0.5, device="cuda")
+    out = torch.zeros(B, n_new, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(cache.n_seq, oc.n_head, 24, dtype=torch.int32, device="cuda")
+    first = cache.table.clone()
+
+    def call(table, table_out):
+        cache.table = table
+        return m.generate_kv8(cache, prompt, n_new, U, out, budget=24, recent=10, table_out=table_out, kept=kept)
+    call(first, other)
+    good = out.clone()
+    bad, bad_other = first.clone(), other.clone()
+    bad[3, 1], bad_other[-1, 0] = cache.k.shape[0], -1
+    for t, o in ((bad, other), (bad, other), (first, bad_other), (first, bad_other)):
+        with pytest.raises(gb.GptError) as e:
+            call(t, o)
+        assert e.value.name == "GPT_ERR_INVALID_ARG"
+        if flags:
+            assert int(cache.flags) == gb.FLAG_BLOCK_RANGE
+            cache.flags.zero_()
+    call(first, other)
+    assert torch.equal(out, good) and (not flags or int(cache.flags) == 0)
+    # a prompt's length is checked at every call too
+    for _ in range(2):
+        cache.table = first
+        with pytest.raises(gb.GptError) as e:
+            m.generate_kv8(cache, prompt, 3, U[:3].contiguous(), torch.zeros(B, 3, dtype=torch.int32, device="cuda"),
+                           prompt_len=dev([9, 1, 1, 1], np.int32))
+        assert e.value.name == "GPT_ERR_INVALID_ARG"
+    m.close()
