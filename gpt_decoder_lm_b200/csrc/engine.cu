@@ -1184,8 +1184,8 @@ gpt_status decode_step_t(gpt_model* m, int t, const Kv8Gen* kv = nullptr) {
 // The kernels and copies of one gpt_generate_kv8 call, enqueued on the model's stream.
 template <typename T>
 static gpt_status generate_kv8_body(gpt_model* m, const Kv8Args& cache, const int32_t* d_prompt,
-                                    const int32_t* d_prompt_len, int32_t T0, int32_t n_new, int32_t budget,
-                                    int32_t recent, const int32_t* d_table_out, int32_t* d_kept,
+                                    const int32_t* d_prompt_len, int32_t T0, int32_t longest, int32_t n_new,
+                                    int32_t budget, int32_t recent, const int32_t* d_table_out, int32_t* d_kept,
                                     const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
                                     const float* d_min_p, const float* d_uniform, int32_t* d_out, float* d_logp) {
   Ctx& c = m->ctx;
@@ -1206,7 +1206,7 @@ static gpt_status generate_kv8_body(gpt_model* m, const Kv8Args& cache, const in
   kv.cache.flags = m->kv8_flags();  // the call's own: it reports them whether or not the cache has a word
   kv.len = m->spos;
   kv.weights = budget > 0;
-  kv.bound = T0;
+  kv.bound = longest;
   const int capacity = cache.max_blocks << cache.lgP;
   const int32_t* other = d_table_out;
   cudaMemsetAsync(cache.len, 0, (size_t)cache.S * 4, c.stream);
@@ -1881,9 +1881,22 @@ gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int3
   if (budget > 0 && (budget >= capacity || recent < 0 || recent > budget || !a.w || !d_table_out ||
                      d_table_out == cache->d_table || !d_kept))
     return fail(m, GPT_ERR_INVALID_ARG, "generate_kv8: eviction needs recent <= budget < capacity, weights and a second table");
+  // Eviction goes by what the longest sequence holds: its prompt's length is asked for (lengths out of range, which the
+  // call refuses later, count as the kernels take them).  Without eviction the bound T0 is enough.
+  int longest = T0;
+  if (budget > 0 && d_prompt_len) {
+    int32_t len[256];
+    longest = 1;
+    for (int b = 0; b < m->B; b += 256) {
+      const int n = std::min(256, m->B - b);
+      cudaMemcpyAsync(len, d_prompt_len + b, (size_t)n * 4, cudaMemcpyDeviceToHost, m->ctx.stream);
+      if (cudaStreamSynchronize(m->ctx.stream) != cudaSuccess) return check_cuda(m, "generate_kv8");
+      for (int i = 0; i < n; i++) longest = std::max(longest, std::min(len[i], T0));
+    }
+  }
   if (h_evictions) {
     int n = 0;
-    for (int i = 1, bound = T0; budget > 0 && i < n_new; i++, bound++)
+    for (int i = 1, bound = longest; budget > 0 && i < n_new; i++, bound++)
       if (bound == capacity) n++, bound = budget;
     *h_evictions = n;
   }
@@ -1892,12 +1905,13 @@ gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int3
                            (uint64_t)(uintptr_t)d_kept, (uint64_t)(uintptr_t)d_temperature, (uint64_t)(uintptr_t)d_top_k,
                            (uint64_t)(uintptr_t)d_top_p, (uint64_t)(uintptr_t)d_min_p, (uint64_t)(uintptr_t)d_uniform,
                            (uint64_t)(uintptr_t)d_out, (uint64_t)(uintptr_t)d_logp};
-  static_assert(16 * 8 + sizeof(gpt_kv8_cache) <= sizeof key, "the key holds the cache");
-  memcpy(&key[16], cache, sizeof *cache);
+  static_assert(17 * 8 + sizeof(gpt_kv8_cache) <= sizeof key, "the key holds the cache");
+  key[16] = (uint64_t)longest;
+  memcpy(&key[17], cache, sizeof *cache);
   s = run_generation(m, key, "generate_kv8", [&] {
-    return m->bf16m ? generate_kv8_body<bf16>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
+    return m->bf16m ? generate_kv8_body<bf16>(m, a, d_prompt, d_prompt_len, T0, longest, n_new, budget, recent, d_table_out, d_kept,
                                               d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp)
-                    : generate_kv8_body<float>(m, a, d_prompt, d_prompt_len, T0, n_new, budget, recent, d_table_out, d_kept,
+                    : generate_kv8_body<float>(m, a, d_prompt, d_prompt_len, T0, longest, n_new, budget, recent, d_table_out, d_kept,
                                                d_temperature, d_top_k, d_top_p, d_min_p, d_uniform, d_out, d_logp);
   });
   if (s == GPT_ERR_CUDA) return s;

@@ -523,8 +523,9 @@ gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, i
  * through the forward once; their keys and values are appended to the cache,
  * and every further token costs one decoding step over it.  Positions go on
  * counting from each prompt's end.
- * budget > 0: when the next token would not fit in the table's capacity
- * (max_blocks * block_tokens), every sequence is brought down to `budget`
+ * budget > 0: when the next token of the longest sequence would not fit in the
+ * table's capacity (max_blocks * block_tokens; the lengths of the prompts are
+ * read before the call's work), every sequence is brought down to `budget`
  * slots (gpt_kv8_evict with `recent`, the weights being accumulated from the
  * prompt on), into the blocks of d_table_out (int32 [n_seq, max_blocks]; blocks
  * of the same pool that d_table does not name), then back, in turn.
@@ -541,9 +542,12 @@ gpt_status gpt_kv8_advance(const gpt_kv8_cache* cache, const int32_t* d_start, i
  * [1, T0] or a block id outside the pool, in either table, where the call came
  * to use it, as GPT_ERR_INVALID_ARG, a bounded wait that ran out as
  * GPT_ERR_TIMEOUT (the outputs are not valid then); the bits are set in
- * cache->d_flags too, where there is one.  Otherwise as gpt_generate: overwrites the activations, synchronising, replayed as a CUDA
- * graph when a call repeats; GPT_ERR_UNSUPPORTED with recompute, or for a
- * head_dim that the cache does not have. */
+ * cache->d_flags too, where there is one.  Otherwise as gpt_generate:
+ * overwrites the activations, synchronising, replayed as a CUDA graph when a
+ * call repeats (with eviction: its longest prompt too; a caller who exchanges
+ * the tables after an odd number of evictions makes another call);
+ * GPT_ERR_UNSUPPORTED with recompute, or for a head_dim that the cache does not
+ * have. */
 gpt_status gpt_generate_kv8(gpt_model* m, const gpt_kv8_cache* cache, const int32_t* d_prompt,
                             const int32_t* d_prompt_len, int32_t T0, int32_t n_new, int32_t budget, int32_t recent,
                             const int32_t* d_table_out, int32_t* d_kept, const float* d_temperature,

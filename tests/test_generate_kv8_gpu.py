@@ -249,3 +249,49 @@ def test_tables_outside_the_pool_are_reported(flags):
                            prompt_len=dev([9, 1, 1, 1], np.int32))
         assert e.value.name == "GPT_ERR_INVALID_ARG"
     m.close()
+
+
+@pytest.mark.parametrize("lens,T0,budget", [([9, 5, 3, 1], 20, 24), ([12, 12, 2, 7], 32, 20)])
+def test_eviction_counts_from_the_longest_prompt(lens, T0, budget):
+    """A buffer wider than its longest prompt: eviction comes when that one's next token does not fit, as the oracle has
+    it, and the number of evictions, the lengths and the kept slots agree."""
+    m, params, oc = setup("char", "fp32")
+    B, P, max_blocks, recent, n_new = oc.batch_size, 16, 2, 6, 40
+    rng = np.random.default_rng(7)
+    prompts = [rng.integers(0, oc.vocab_size, n) for n in lens]
+    padded = np.full((B, T0), -5)
+    for b, p in enumerate(prompts):
+        padded[b, :len(p)] = p
+    U = rng.random((n_new, B)).astype(np.float32)
+    cache, other = make_cache(oc, P, max_blocks)
+    first = cache.table
+    kept = torch.full((cache.n_seq, oc.n_head, budget), -1, dtype=torch.int32, device="cuda")
+    out = torch.full((B, n_new), -1, dtype=torch.int32, device="cuda")
+    plen, prompt, uniform = dev(lens, np.int32), dev(padded, np.int32), dev(U, np.float32)
+
+    def call():
+        cache.table = first
+        return m.generate_kv8(cache, prompt, n_new, uniform, out, prompt_len=plen, budget=budget, recent=recent,
+                              table_out=other, kept=kept)
+    n = call()
+    d = O.Decoder(oc, params, prompts, P, max_blocks, budget, recent)
+    got = out.cpu().numpy()
+    for i in range(n_new - 1):
+        d.step(got[:, i])
+    assert n == d.evictions and n > 0
+    assert cache.length.cpu().numpy().tolist() == np.concatenate([c.length for c in d.layers]).tolist()
+    sure = (np.array(d.margins).reshape(n, oc.n_layer, B, oc.n_head) > 1e-3).all(0)
+    ref = np.stack(d.kept)
+    assert (kept.cpu().numpy().reshape(ref.shape) == ref).all(-1)[sure].all() and sure.mean() > 0.9
+    # other lengths in the same buffers are another call, not a replay of this one
+    for _ in range(2):
+        assert call() == n
+    plen.copy_(dev([T0, 1, 2, 3], np.int32))
+    prompt.copy_(dev(rng.integers(0, oc.vocab_size, (B, T0)), np.int32))
+    longer, bound = 0, T0
+    for _ in range(n_new - 1):
+        if bound == max_blocks * P:
+            longer, bound = longer + 1, budget
+        bound += 1
+    assert call() == longer != n
+    m.close()
