@@ -728,9 +728,11 @@ class KV8Cache:
                 budget, recent, kept.data_ptr())
 
     def advance(self, start=None, n_rows=None, max_new=1, max_len=0):
-        """gpt_kv8_advance: the lengths grow by the step's rows (n_rows: one for each sequence where None)."""
-        _run_on(self._index, self._lib.gpt_kv8_advance, "kv8_advance", self._ref, self._start(start),
-                self.n_seq if n_rows is None else n_rows, max_new, max_len)
+        """gpt_kv8_advance: the lengths grow by the step's rows.  n_rows None: with start, as many as it says (give the
+        arrays' own number where append was to leave out offsets past it); without, one for each sequence."""
+        if n_rows is None:
+            n_rows = self.n_seq if start is None else 2 ** 31 - 1
+        _run_on(self._index, self._lib.gpt_kv8_advance, "kv8_advance", self._ref, self._start(start), n_rows, max_new, max_len)
 
 
 def test_gemm(backend, M, N, K, A, lda, a_kmajor, B, ldb, b_kmajor, epi_kind, act=0, out=None, out2=None, ldo=0,

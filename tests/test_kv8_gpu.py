@@ -864,3 +864,16 @@ def test_a_heavy_slot_over_a_long_flat_tail_in_fp32(hd, P, G, n, z, max_len):
     err = float((out.double() - want).abs().max())
     assert err <= tol, (err, tol)
     assert float((lse.double() - (z64 + torch.log1p(e))).abs().max()) <= B * 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -23 * (B + 11)
+
+
+def test_advance_by_offsets_alone():
+    """Rows of different numbers, without the number of all rows: the lengths grow by the offsets' differences, as the
+    other calls take them."""
+    gpu, _, _ = make(25, [40, 40, 40], 1, 32, 16, extra=64)
+    gpu.length.copy_(torch.tensor([5, 0, 7], dtype=torch.int32))
+    gpu.advance(start=dev(starts([30, 0, 12])), max_new=30)
+    assert gpu.length.tolist() == [35, 0, 19] and int(gpu.flags) == 0
+    gpu.advance(start=dev(starts([1, 1, 1])))
+    assert gpu.length.tolist() == [36, 1, 20] and int(gpu.flags) == 0
+    gpu.advance(start=dev(starts([2, 1, 1])))  # more than max_new
+    assert gpu.length.tolist() == [36, 2, 21] and int(gpu.flags) == gb.FLAG_ROW_RANGE
