@@ -112,7 +112,7 @@ struct Aside {
     x[i] = y;
   }
 };
-// Their sums of weights carry what an addition rounds off (Kahan): equal weights would round the same way each time.
+// The sums of weights carry what an addition rounds off (Kahan): equal weights would round the same way each time.
 __device__ __forceinline__ void add_kept(float& sum, float& off, float x) {
   const float y = x - off, t = sum + y;
   off = (t - sum) - y;
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
           fo[nt][e] = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[nt][e] - mv1);
           m[nt][e] = m1, mv[nt][e] = mv1;
           l[nt][e] *= fl;
-          if (TERMS == 2) l_off[nt][e] *= fl;
+          l_off[nt][e] *= fl;
 #pragma unroll
           for (int i = 0; i < MT; i++) o[i][nt][e] *= fo[nt][e], o[i][nt][2 + e] *= fo[nt][e];
         }
@@ -601,22 +601,20 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
         c[0][e] = v_factor(v0 + d);
         c[1][e] = v0 == v1 ? c[0][e] : v_factor(v1 + d);
       }
-      float lt[2] = {0.f, 0.f};  // fp32 rows: the tile's sums
+      float lt[2] = {0.f, 0.f};  // the tile's sums
 #pragma unroll
       for (int gr = 0; gr < 2; gr++)
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           const float x = sfu_exp2(sc[gr][nt][2 * half] - mm[0]), y = sfu_exp2(sc[gr][nt][2 * half + 1] - mm[1]);
-          (TERMS == 2 ? lt[0] : l[nt][0]) += x;
-          (TERMS == 2 ? lt[1] : l[nt][1]) += y;
+          lt[0] += x;
+          lt[1] += y;
           const uint32_t v = pack_f16(x * c[gr][0], y * c[gr][1]);
           p[gr][nt][half] = transpose8(v);
           if (TERMS == 2) plo[gr][nt][half] = transpose8(pack_p_rest(x * c[gr][0], y * c[gr][1], v));
         }
-      if (TERMS == 2) {
-        add_kept(l[nt][0], l_off[nt][0], lt[0]);
-        add_kept(l[nt][1], l_off[nt][1], lt[1]);
-      }
+      add_kept(l[nt][0], l_off[nt][0], lt[0]);
+      add_kept(l[nt][1], l_off[nt][1], lt[1]);
     }
     // ---- o += v^T p^T
     bool poison = false;
@@ -705,7 +703,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
-      float x = TERMS == 2 ? l[nt][e] - l_off[nt][e] : l[nt][e];
+      float x = l[nt][e] - l_off[nt][e];
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int r = 8 * nt + 2 * t + e;
@@ -1018,7 +1016,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
         fo[half] = mv1 == -INFINITY ? 1.f : sfu_exp2(mv[half] - mv1);
         m[half] = m1, mv[half] = mv1;
         l[half] *= fl;
-        if (TERMS == 2) l_off[half] *= fl;
+        l_off[half] *= fl;
 #pragma unroll
         for (int i = 0; i < HD / 8; i++) o[i][2 * half] *= fo[half], o[i][2 * half + 1] *= fo[half];
       }
@@ -1027,7 +1025,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
         for (int i = 0; i < HD / 8; i++) aside.scale(i, fo[0], fo[0], fo[1], fo[1]);
       }
     }
-    float mm[2], dv[2], lt[2] = {0.f, 0.f};  // fp32 rows: the tile's sums
+    float mm[2], dv[2], lt[2] = {0.f, 0.f};  // (lt: the tile's sums)
 #pragma unroll
     for (int half = 0; half < 2; half++) {
       mm[half] = m[half] == -INFINITY ? 0.f : m[half];
@@ -1041,8 +1039,8 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
       for (int x = 0; x < 2; x++) {
         const float e0 = sfu_exp2(sc[2 * kk + x][0] - mm[0]), e1 = sfu_exp2(sc[2 * kk + x][1] - mm[0]);
         const float e2 = sfu_exp2(sc[2 * kk + x][2] - mm[1]), e3 = sfu_exp2(sc[2 * kk + x][3] - mm[1]);
-        (TERMS == 2 ? lt[0] : l[0]) += e0 + e1;
-        (TERMS == 2 ? lt[1] : l[1]) += e2 + e3;
+        lt[0] += e0 + e1;
+        lt[1] += e2 + e3;
         p[2 * x] = pack_f16(e0 * c0, e1 * c0);
         p[2 * x + 1] = pack_f16(e2 * c1, e3 * c1);
         if (TERMS == 2) {
@@ -1062,10 +1060,8 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
         mma(o[i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
       }
     }
-    if (TERMS == 2) {
-      add_kept(l[0], l_off[0], lt[0]);
-      add_kept(l[1], l_off[1], lt[1]);
-    }
+    add_kept(l[0], l_off[0], lt[0]);
+    add_kept(l[1], l_off[1], lt[1]);
     if (poison) {  // the NaN that were taken out go into the rows that see them
       for (int row = 0; row < MT; row++) {
         const int j = tile * MT + row;
@@ -1094,7 +1090,7 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 
 #pragma unroll
   for (int half = 0; half < 2; half++) {
-    if (TERMS == 2) l[half] -= l_off[half];
+    l[half] -= l_off[half];
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
   }
@@ -1447,7 +1443,7 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
         const float fl = m1 == -INFINITY ? 1.f : sfu_exp2(m - m1), fo = mv1 == -INFINITY ? 1.f : sfu_exp2(mv - mv1);
         m = m1, mv = mv1;
         l *= fl;
-        if (S::TERMS == 2) l_off *= fl;
+        l_off *= fl;
         if (j > 0) {
           // O holds the products of the tiles before.  S of this tile was issued after P V of tile j - 2, so that of
           // tile j - 1 is the only one that may be in flight.
@@ -1493,7 +1489,7 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
         }
         tmem_st_wait();
       }
-      float lt = 0.f;  // fp32 rows: the tile's sum
+      float lt = 0.f;  // the tile's sum
       const float mm = m == -INFINITY ? 0.f : m, dv = mm - (mv == -INFINITY ? 0.f : mv);
 #pragma unroll
       for (int half = 0; half < 2; half++) {
@@ -1505,7 +1501,7 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
           for (int i = 0; i < 16; i += 2) {
             const float e0 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i]), f[2 * half + g], -mm));
             const float e1 = sfu_exp2(fmaf(__uint_as_float(v[half][16 * g + i + 1]), f[2 * half + g], -mm));
-            (S::TERMS == 2 ? lt : l) += e0 + e1;
+            lt += e0 + e1;
             pk[8 * g + i / 2] = pack_f16(e0 * c, e1 * c);
             if (S::TERMS == 2) pl[8 * g + i / 2] = pack_p_rest(e0 * c, e1 * c, pk[8 * g + i / 2]);
           }
@@ -1514,7 +1510,7 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
         tmem_st_32x32b_x16(trow + 64 * u + 16 * half, pk);
         if (S::TERMS == 2) tmem_st_32x32b_x16(trow + 64 * u + 32 + 16 * half, pl);
       }
-      if (S::TERMS == 2) add_kept(l, l_off, lt);
+      add_kept(l, l_off, lt);
       tmem_st_wait();
       bool nan = false;
 #pragma unroll
@@ -1562,7 +1558,7 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
 #pragma unroll
       for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     }
-    sh.stats.m[r] = m, sh.stats.mv[r] = mv, sh.stats.l[r] = S::TERMS == 2 ? l - l_off : l;
+    sh.stats.m[r] = m, sh.stats.mv[r] = mv, sh.stats.l[r] = l - l_off;
   }
   tc_fence_before();
   __syncthreads();

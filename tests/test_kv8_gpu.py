@@ -877,3 +877,30 @@ def test_advance_by_offsets_alone():
     assert gpu.length.tolist() == [36, 1, 20] and int(gpu.flags) == 0
     gpu.advance(start=dev(starts([2, 1, 1])))  # more than max_new
     assert gpu.length.tolist() == [36, 2, 21] and int(gpu.flags) == gb.FLAG_ROW_RANGE
+
+
+@pytest.mark.parametrize("max_len", [0, 1])
+@pytest.mark.parametrize("z", [6.0, 12.0])
+@pytest.mark.parametrize("hd,P,G,n", [(64, 16, 1, 1), (128, 64, 4, 1), (32, 16, 2, 5), (64, 16, 1, 40), (32, 32, 2, 20),
+                                      (64, 16, 1, 100), (128, 16, 5, 27)])
+def test_the_sum_of_weights_over_a_long_flat_tail_in_bf16(hd, P, G, n, z, max_len):
+    """The log-sum-exp of bf16 rows is an fp32 output, and the accumulated weights go by it: one slot z nats above 40,000
+    equal ones, whose weights all round alike when they are added.  |lse - lse64| <= B 2^-21 + 2^-20 + 2^-23 |lse| with
+    B = z, |o - o64| <= 2^-10 V + 2^-8 |o64|, as in the other cases."""
+    tail = 40000
+    blocks = -(-(tail + 1 + n) // P)
+    c = gb.KV8Cache.allocate(1, 1, hd, P, blocks)
+    c.length.fill_(tail)
+    c.v.fill_(0x38)  # 1.0 everywhere but for the heavy slot's 0
+    c.v[0, :, 0] = 0
+    c.k[0, 0, 0, 0] = 0x38
+    c.k_scale.fill_(1.0), c.v_scale.fill_(1.0)
+    q = torch.zeros(n, G, hd, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 0] = z
+    out, lse = torch.zeros_like(q), torch.zeros(n, G, device="cuda")
+    c.attention(q, out, start=dev(starts([n])), max_new=n, lse=lse, scale=1.0, max_len=max_len)
+    e = np.exp(-z) * (tail + torch.arange(n, device="cuda", dtype=torch.float64))[:, None]
+    err = float((lse.double() - (z + torch.log1p(e))).abs().max())
+    assert err <= z * 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -23 * (z + 5), err
+    want = (e / (1 + e))[..., None]
+    assert ((out.double() - want).abs() <= 2.0 ** -10 + 2.0 ** -8 * want).all()
