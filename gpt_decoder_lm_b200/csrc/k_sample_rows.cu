@@ -84,9 +84,9 @@ struct Scale {
   double cd;      // log2(e) / temperature
   __device__ __forceinline__ void set(float top, float temperature) {
     zf = top;
-    cd = 1.4426950408889634074 / (double)temperature;
+    cd = 1.4426950408889634074 / (double)fmaxf(temperature, 0x1p-122f);  // cf in fp32's range
     half = 48.0 / cd < 1.7e38 ? 1.f : 0.5f;  // (cd may be 0)
-    cf = fminf((float)(cd * 32.0 / half), 3.0e38f);
+    cf = (float)(cd * 32.0 / half);
   }
   __device__ __forceinline__ double dist(float z) const { return ((double)zf - (double)z) * cd; }
   // rint(32 y) in fp32, of a logit not below floor(48); both roundings keep the order of logits.  *fr: 32 y - bin.

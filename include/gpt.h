@@ -388,7 +388,8 @@ gpt_status gpt_sample(const void* d_logits, int32_t logits_bf16, int32_t rows, i
 /* gpt_sample with parameters for each row, and min-p.  d_temperature,
  * d_top_k, d_top_p, d_min_p: device arrays [rows], each nullable (1, off, off,
  * off).  For a row, in this order:
- *   temperature not > 0   greedy: the arg-max, lowest index on ties
+ *   temperature not > 0   greedy: the arg-max, lowest index on ties (between 0
+ *                         and 2^-122 it counts as 2^-122)
  *   0 < top_k < V         keeps the logits >= the k-th largest (ties kept)
  *   top_p < 1             of those, keeps p >= tau for the largest tau whose
  *                         kept mass reaches top_p of theirs (<= 0: the maximum)

@@ -189,3 +189,22 @@ def test_temperatures_at_which_the_whole_range_of_logits_counts(V, dtype):
             par = {"temperature": np.full(rows, t, np.float32), "top_k": np.full(rows, k, np.int32),
                    "top_p": np.full(rows, p, np.float32), "min_p": np.full(rows, m, np.float32)}
             check(z, par, rng.random(rows).astype(np.float32))
+
+
+def test_the_smallest_temperatures():
+    """Temperatures below 2^-122 count as 2^-122, for logits so close that it matters; for others the largest is drawn."""
+    rng = np.random.default_rng(11)
+    rows, V = 16, 3001
+    z = (rng.uniform(-1, 1, (rows, V)) * 2.0 ** -121).astype(np.float32)
+    z[8:] = rng.standard_normal((8, V))
+    u, floor = rng.random(rows).astype(np.float32), np.float32(2.0 ** -122)
+    for t in (2.0 ** -122, 1e-37, 1e-38, 1e-45):
+        for k, p, m in ((0, 1.0, 0.0), (40, 1.0, 0.0), (0, 0.5, 0.0), (V // 2, 0.9, 0.1)):
+            par = {"temperature": np.full(rows, t, np.float32), "top_k": np.full(rows, k, np.int32),
+                   "top_p": np.full(rows, p, np.float32), "min_p": np.full(rows, m, np.float32)}
+            got, lp = draw(torch.from_numpy(z).cuda(), par, u)
+            for r in range(rows):
+                tok, ref = S.sample_row_minp(z[r].astype(np.float64), float(floor), k, float(par["top_p"][r]),
+                                             float(par["min_p"][r]), float(u[r]))
+                assert got[r] == tok, (t, k, p, m, r)
+                assert abs(lp[r] - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -32
