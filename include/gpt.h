@@ -478,10 +478,11 @@ gpt_status gpt_kv8_append(const gpt_kv8_cache* cache, const int32_t* d_start, in
  * none of whose blocks is in the pool gives zeros and -infinity.  max_len: a
  * bound on len + n that the caller knows (0: the table's capacity); it decides
  * how the work is split, not what is read.  fp32 rows are computed to fp32
- * accuracy: a weight to 2^-21 of itself, however small it is beside the
- * largest (a score's rounding, 2^-21 of scale sum |q k|, moves it as much), and
- * sums that leave about 1e-6 of the outputs' norm over any number of slots;
- * bf16 rows to fp16's, below bf16's. */
+ * accuracy: a weight to 2^-21 of itself (a score's rounding, 2^-21 of scale
+ * sum |q k|, moves it as much), or of itself times its value block's scale to
+ * 2^-43 of the largest such product, and sums that leave about 1e-6 of the
+ * outputs' norm over any number of slots; bf16 rows to fp16's, below bf16's
+ * (2^-32 of the largest product).  lse is fp32 for both. */
 gpt_status gpt_kv8_attention(const gpt_kv8_cache* cache, const int32_t* d_start, int32_t n_rows, int32_t max_new,
                              int32_t n_head, int32_t rows_bf16, const void* d_q, int64_t q_ld, float scale,
                              int32_t max_len, void* d_out, int64_t out_ld, float* d_lse, void* cuda_stream);
