@@ -86,8 +86,8 @@ constexpr int AU = 4;  // units of 8 elements that a thread holds: 512 threads c
 // head, of K or of V (grid: touched block, 2 H, sequence).  HBM-bound: the
 // rows are read once, held as they came, and quantised after the block's
 // maximum is known.  B200: 6800 bf16 tokens of 25 heads of 64 in 15.5 us, 65% of
-// the copy bandwidth (reads and writes do not overlap within a block); one token
-// for each of 12 sequences 2.7 us, a launch.
+// the copy bandwidth (reads and writes do not overlap within a block), fp32 in 21.9
+// us, 77%; one token for each of 12 sequences 2.7 us, a launch.
 template <typename T, int HD>
 __global__ void __launch_bounds__(512) k_kv8_append(Kv8Args a, const T* __restrict__ xk, long k_ld,
                                                     const T* __restrict__ xv, long v_ld, int vec) {

@@ -359,11 +359,13 @@ __device__ __forceinline__ void join_blocks(RowStats<ROWS>& st, const float* par
 // at the end in a fixed order.
 //
 // B200: 6 sequences of 20000 to 40000 slots, 32 on 8 heads of 128: 66 us, 86%
-// of the copy bandwidth.  64 sequences of up to 1023 slots, 12 heads of 64: 19.0
-// us (8.6 us at the copy bandwidth): about 3 us pass before the first tile (start,
-// length, table, codes), a warp's tile of 32 slots takes some 540 cycles of its
-// scheduler (64 conversions at 2, 16 MMA at 12.5, the rest softmax), and SMs with
-// longer sequences finish last.
+// of the copy bandwidth (fp32 rows, twice the MMA: 94 us).  64 sequences of up to
+// 1023 slots, 12 heads of 64: 19.5 us (8.6 us at the copy bandwidth; fp32 25 us).
+// A warp's tile of 32 slots takes some 540 cycles of its scheduler (64 conversions
+// at 2, 16 MMA at 12.5, the rest softmax), which for all tiles over all schedulers
+// is 6.7 us; about 3 us pass before the first tile (start, length, table, codes)
+// and 2 in the join; the rest is uneven work: one block a (sequence, head) whatever
+// its length, 768 on 740 places, so that an SM takes what its five happen to hold.
 template <typename T, int HD, int NT, int NW, int NS, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs at) {
   constexpr int ROWS = 8 * NT, TERMS = sizeof(T) == 4 ? 2 : 1;
@@ -753,10 +755,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) k_kv8_attn(Kv8Args a, AttnArgs 
 // meanwhile; two tiles alternate, so that one barrier a tile is enough.  The
 // statistics are those of k_kv8_attn.
 //
-// B200, 63 to 200 rows over up to 1501 slots, 4 sequences of 25 heads of 64: 33 us
-// (43 us with 16 rows a block and the conversions in every warp).  A warp's tile
-// of 64 slots is 64 MMA at 12.5 cycles; three blocks an SM keep the pipe 80% busy
-// between a prologue and a join of together a third of a block's time.
+// For 17 to 48 rows (fp32: 64) of 64 or fewer dimensions.  B200, 20 to 40 rows over
+// up to 1501 slots, 4 sequences of 25 heads of 64: 19 us (fp32 27 us), 500 blocks
+// on 444 places; barriers and the first loads (2.8 and 1.7 cycles an issued
+// instruction) bound it, not the MMA: a prologue and a join are a third of a
+// block's time, and with half of the rows in use the pipe is 8% busy.
 constexpr int MR = 64, MW = 4, MT = 64;  // rows and warps of a block, slots of a tile
 
 template <int HD>
@@ -1124,13 +1127,14 @@ __global__ void __launch_bounds__(MW * 32, MINB) k_kv8_attn_many(Kv8Args a, Attn
 // where sums left in the tensor core drift off by 2.7e-6.
 //
 // B200: 2 sequences of 900 to 1000 new rows over 3000 to 4000 slots, 16 heads of
-// 64: 100 us, 310 TFLOP/s of the visible products (the warp MMA's blocks of 64
-// rows: 203 us).  Two resident blocks keep the SFU and the schedulers of the
+// 64: 102 us, 302 TFLOP/s of the visible products (the warp MMA's blocks of 64
+// rows: 203 us; fp32 rows 157 us).  Two resident blocks keep the SFU and the schedulers of the
 // softmax warps busy: a tile is 8192 exponentials at 16 a cycle and SM, and about
 // five other instructions each.  63 to 200 new rows over up to 1501 slots, 4
 // sequences of 25 heads: 28 us (33 us), two fifths of it before the first tile
-// and in the join.  fp32, 3 sequences of 71 new rows over 4300 slots, 8 heads of
-// 128: 68 us (with two converting warps 81 us, the warp MMA's blocks 100 us).
+// and in the join (fp32 39 us).  fp32, 3 sequences of 71 new rows over 4300 slots,
+// 8 heads of 128: 66 us (with two converting warps 81 us, the warp MMA's blocks
+// 100 us).
 constexpr int CR = 128, CT = 64;             // rows of a block, slots of a tile
 constexpr int C_SOFT = 4;                    // softmax warps; one more issues, others convert
 
@@ -1576,6 +1580,13 @@ __global__ void __launch_bounds__((TcShape<T, HD>::THREADS), (TcShape<T, HD>::MI
 // the product's 16-row operand, converted once, and all rows pass by: 64 at a
 // time as fp16 in shared memory, made once for the block's four warps while the
 // tile before is used.  k_kv8_accumulate_few has the rows in registers.
+//
+// B200, 63 to 200 rows over up to 1501 slots, 4 sequences of 25 heads of 64: 17.6 us
+// (fp32 29 us) on a floor of 1.3; 130 rows over 3000 slots, 6 sequences of 8 heads
+// of 128: 59 us (fp32 110 us) on 3.5.  Bound by the warp MMA and what feeds it: the
+// pipe is 20 to 28% busy, every block scales and converts all rows of q again, and
+// the rows are not divided over blocks (500 rows on one head of 128 dimensions,
+// 3000 slots: 24 blocks, 21 us, fp32 46 us).
 constexpr int AR = 64, AT = 128;  // rows a tile, slots a block
 
 // Where dimension d of a row lies so that the 16 x 8 x 16 MMA, which takes a row's halves in order, meets the
@@ -1766,8 +1777,9 @@ __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_many(Kv8Args a, At
 // At most 8 NT rows (a decoding step): their operand is made once, and each warp
 // of a (sequence, head) takes every so-manieth tile of 32 tokens, with the next
 // tile's codes on their way and the block ids of the one behind it looked up.
-// B200: long contexts (as k_kv8_attn's) 38.5 us, 79% of the copy bandwidth; the
-// batch 12.9 us (4.8 us at the copy bandwidth), of which 4 us before the first tile.
+// B200: long contexts (as k_kv8_attn's) 38.5 us, 79% of the copy bandwidth (fp32
+// rows 43 us); the batch 13 us (4.8 us at the copy bandwidth; fp32 15 us): 4 us
+// before the first tile, then uneven work as k_kv8_attn's.
 template <typename T, int HD, int NT, int MINB>
 __global__ void __launch_bounds__(128, MINB) k_kv8_accumulate_few(Kv8Args a, AttnArgs at) {
   constexpr int KS = HD / 16;
@@ -1965,9 +1977,11 @@ bool launch_attn_rows(Ctx& c, const Kv8Args& a, const AttnArgs& at, int max_len)
   if (rows <= 8 && pairs * 8 <= c.num_sms) return launch_attn<T, HD, 1, NS, 1, 8>(c, a, at, max_len);
   if (rows <= 8) return launch_attn<T, HD, 1, NS, HD == 128 ? 3 : HD == 64 && sizeof(T) == 2 ? 5 : 4>(c, a, at, max_len);
   if (rows <= 16) return launch_attn<T, HD, 2, NS, HD == 128 ? 2 : sizeof(T) == 2 ? 4 : 3>(c, a, at, max_len);
-  // By trial: 20 to 48 rows (fp32: 64, one block) of 64 or fewer dimensions take up to 25% less with the warp MMA's blocks
-  // of 64 rows; of 128 dimensions, and above, tcgen05 takes less (bf16: 64 rows 24.7 us against 27.9, 1000 rows half;
-  // fp32: 100 rows of 30 sequences 65.9 us against 90.1, 71 rows of 128 dimensions 67 against 100).
+  // By trial (warp MMA's blocks of 64 rows against tcgen05): 20 to 48 rows of 64 or fewer dimensions mostly take less with
+  // the former (bf16, 4 sequences of 25 heads of 64, 32 rows 24 us against 29; 2 of 8 heads of 32 12.6 against 18.3; but 30 of
+  // 8 heads of 64 34 against 32), fp32 rows to 64, one block, where there are few blocks (one sequence of 12 heads 28 us
+  // against 30, 2 of 8 heads of 32 15.5 against 23.1; 30 of 8 heads 55 against 46).  Above, and of 128 dimensions, tcgen05
+  // takes less (100 rows of 30 sequences of 8 heads of 64: bf16 36 us against 63, fp32 52 against 98).
   if constexpr (HD == 128) {
     return launch_attn_tc<T, HD>(c, a, at, max_len);
   } else {
