@@ -82,7 +82,8 @@ struct Exact {
     for (int i = 0; i < 4; i++) d[i] += x[i];
   }
 };
-// Their outputs add up in the tensor cores over CHAIN slots; then they are added, rounded, to sums set aside, so that there are few roundings of either kind over a long context.
+// Their outputs add up in the tensor cores over CHAIN slots; then they are added, rounded, to sums set aside, so that
+// there are few roundings of either kind over a long context.
 constexpr int CHAIN = 256;
 // The warp MMA's sums set aside, four to an index, in the thread's local memory: they are touched once in a chain, and
 // registers and shared memory decide how many warps run.  (In shared memory, 16 KB more a block of 128 dimensions, two
@@ -119,8 +120,9 @@ __device__ __forceinline__ void add_kept(float& sum, float& off, float x) {
   sum = t;
 }
 
-// A V block's factor of the weights (2^P_LOG2 among it), from its log2.  Past 2^120 (a block far above the one whose values set the running
-// maximum of scores + log2(V scale): all its weights have underflowed) it stays finite, so that they remain 0.
+// A V block's factor of the weights (2^P_LOG2 among it), from its log2.  Past 2^120 (a block far above the one whose
+// values set the running maximum of scores + log2(V scale): all its weights have underflowed) it stays finite, so that
+// they remain 0.
 __device__ __forceinline__ float v_factor(float log2) { return sfu_exp2(fminf(log2 + P_LOG2, 120.f)); }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
